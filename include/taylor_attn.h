@@ -219,6 +219,67 @@ TAYLOR_API int taylor_attn_centred_prefill_f32(const float* q, const float* k, c
 TAYLOR_API int taylor_attn_state_merge(const float* a, const float* b, float* out, int B, int H,
                             int d_k, int d_v, int n, cudaStream_t stream);
 
+/* Norms of queries and keys for each head with the position rotation in the
+ * same pass: what the attention calls expect of q and k (unit norm, head-major)
+ * from what a projection gives (token-major).  Per head row x of d entries,
+ *     u = w (.) x / sqrt(sum x^2 + eps),   y = R(p) u,
+ * R(p) turning the first `rot` entries: the pair of frequency freqs[j] is
+ * rotated by the angle p * freqs[j]; pairs are (j, j + rot/2), or
+ * (2j, 2j + 1) with interleaved != 0.  With eps 0 a row of zeros gives zeros.
+ * q is [B][N][Hq][d] and k [B][N][Hk][d], bf16 (the _f32 variant: fp32) with
+ * the strides q_strides, k_strides: HOST arrays of three (batch, token, head)
+ * in elements, >= 0, the d entries contiguous; a slice of a packed projection
+ * is one.  q_out [B][Hq][N][d] and k_out [B][Hk][N][d] are dense, of the same
+ * type; they must not overlap the inputs.  q_weight, k_weight: fp32 [d] or
+ * NULL (ones).  positions: int64 [B][N] on the device, or NULL for pos0 + n.
+ * freqs: HOST array of rot/2 frequencies in radians per position (read before
+ * the call returns), NULL when rot is 0.  Angles are reduced in fp64, sums
+ * are fp32.  1 <= d <= 64, rot even and <= d, eps finite and >= 0; Hq or Hk
+ * may be 0 (that side is left out).  Pointers need the alignment of their
+ * elements only; rows whose length, strides and alignment allow it are moved
+ * in up to 16-byte pieces.  For single tokens N = 1 gives [B][H][1][d], the
+ * decode calls' layout.  No workspace. */
+TAYLOR_API int taylor_attn_qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
+                                        const int64_t* positions, int64_t pos0, const double* freqs, int rot,
+                                        int interleaved, void* q_out, void* k_out, int B, int N, int Hq, int Hk,
+                                        int d, const int64_t* q_strides, const int64_t* k_strides, float eps,
+                                        cudaStream_t stream);
+
+/* taylor_attn_qk_norm_rope with fp32 q, k and outputs. */
+TAYLOR_API int taylor_attn_qk_norm_rope_f32(const float* q, const float* k, const float* q_weight,
+                                            const float* k_weight, const int64_t* positions, int64_t pos0,
+                                            const double* freqs, int rot, int interleaved, float* q_out,
+                                            float* k_out, int B, int N, int Hq, int Hk, int d,
+                                            const int64_t* q_strides, const int64_t* k_strides, float eps,
+                                            cudaStream_t stream);
+
+/* Gradient of taylor_attn_qk_norm_rope: from its inputs and the gradients
+ * dq_out, dk_out of its outputs (dense, as q_out, k_out), the gradients dq, dk
+ * of q and k with the strides dq_strides, dk_strides (as q_strides; every
+ * element at its own address) and, where not NULL, dq_weight and dk_weight
+ * (fp32 [d]; only with that weight), summed over tokens and heads in fp32 in
+ * an order that depends on the sizes alone.  The norm is recomputed from q and
+ * k; a row of zeros with eps 0 has a zero gradient.  Workspace for the weight
+ * gradients' partial sums as taylor_attn_prefill takes it. */
+TAYLOR_API int taylor_attn_qk_norm_rope_backward(const void* q, const void* k, const void* dq_out,
+                                                 const void* dk_out, const float* q_weight, const float* k_weight,
+                                                 const int64_t* positions, int64_t pos0, const double* freqs,
+                                                 int rot, int interleaved, void* dq, void* dk, float* dq_weight,
+                                                 float* dk_weight, int B, int N, int Hq, int Hk, int d,
+                                                 const int64_t* q_strides, const int64_t* k_strides,
+                                                 const int64_t* dq_strides, const int64_t* dk_strides, float eps,
+                                                 cudaStream_t stream);
+
+/* taylor_attn_qk_norm_rope_backward with fp32 tensors. */
+TAYLOR_API int taylor_attn_qk_norm_rope_backward_f32(const float* q, const float* k, const float* dq_out,
+                                                     const float* dk_out, const float* q_weight,
+                                                     const float* k_weight, const int64_t* positions, int64_t pos0,
+                                                     const double* freqs, int rot, int interleaved, float* dq,
+                                                     float* dk, float* dq_weight, float* dk_weight, int B, int N,
+                                                     int Hq, int Hk, int d, const int64_t* q_strides,
+                                                     const int64_t* k_strides, const int64_t* dq_strides,
+                                                     const int64_t* dk_strides, float eps, cudaStream_t stream);
+
 /* taylor_attn_prefill_f32 for callers that cannot allocate device memory
  * (a plugin whose host framework owns all device memory, a serving loop that
  * reserves memory up front and must not see an allocation fail mid-step).

@@ -1,0 +1,51 @@
+// Host helpers of the entry points that check their arguments beside their
+// kernels: alignment, status codes and the strides of strided operands.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/taylor_attn.h"
+
+namespace ta {
+namespace entry {
+
+inline bool aligned(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+inline int status(cudaError_t e) {
+    if (e == cudaSuccess) return TAYLOR_OK;
+    cudaGetLastError();
+    return e == cudaErrorMemoryAllocation ? TAYLOR_ERR_OUT_OF_MEMORY : TAYLOR_ERR_CUDA;
+}
+
+inline int num_sms() {
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    return sms > 0 ? sms : 148;
+}
+
+// Whether an output of these sizes and strides (elements) has every element
+// at an address of its own: the sizes nest in the order of the strides.
+// The innermost run of `row` elements is contiguous.
+template <int K>
+inline bool disjoint(const int64_t (&size)[K], const int64_t (&stride)[K], int64_t row) {
+    int order[K];
+    for (int i = 0; i < K; ++i) order[i] = i;
+    for (int i = 1; i < K; ++i)
+        for (int j = i; j > 0 && stride[order[j]] < stride[order[j - 1]]; --j) {
+            const int t = order[j];
+            order[j] = order[j - 1];
+            order[j - 1] = t;
+        }
+    int64_t extent = row;
+    for (int i = 0; i < K; ++i) {
+        const int64_t n = size[order[i]], s = stride[order[i]];
+        if (n <= 1) continue;
+        if (s < extent) return false;
+        extent = s * (n - 1) + extent;
+    }
+    return true;
+}
+
+}  // namespace entry
+}  // namespace ta

@@ -8,6 +8,7 @@ C names; shape arguments (B, H, N, d_k, d_v) are read from the tensors.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -31,6 +32,8 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _I64 = ctypes.c_int64
+_QK = [_P, _P, _P, _I64, _P, _I, _I]    # q_weight, k_weight, positions, pos0, freqs, rot, interleaved
+_SIZES = [_I] * 5                       # B, N, Hq, Hk, d
 SIGNATURES = {
     "taylor_attn_strerror": (ctypes.c_char_p, [_I]),
     "taylor_attn_version": (_I, []),
@@ -49,6 +52,12 @@ SIGNATURES = {
     "taylor_attn_centred_prefill": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "taylor_attn_centred_prefill_f32": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "taylor_attn_state_merge": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "taylor_attn_qk_norm_rope": (_I, [_P, _P, *_QK, _P, _P, *_SIZES, _P, _P, _F, _P]),
+    "taylor_attn_qk_norm_rope_f32": (_I, [_P, _P, *_QK, _P, _P, *_SIZES, _P, _P, _F, _P]),
+    "taylor_attn_qk_norm_rope_backward":
+        (_I, [_P, _P, _P, _P, *_QK, _P, _P, _P, _P, *_SIZES, _P, _P, _P, _P, _F, _P]),
+    "taylor_attn_qk_norm_rope_backward_f32":
+        (_I, [_P, _P, _P, _P, *_QK, _P, _P, _P, _P, *_SIZES, _P, _P, _P, _P, _F, _P]),
     "taylor_attn_prefill_f32_noalloc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "taylor_attn_prefill_noalloc_scratch_floats": (_I64, []),
     "taylor_attn_device_errors": (_I, [_I, _P]),
@@ -115,6 +124,39 @@ def _need(t: torch.Tensor, name: str, dtype, device=None, shape=None) -> None:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, stream):
+    """Context in which t's device is the current one and `stream` (None: that
+    device's current stream) its current stream, so that what is allocated in
+    it belongs to the stream the kernels run on."""
+    if not t.is_cuda:
+        raise ValueError("the tensors must be CUDA tensors")
+    if stream is None:
+        return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
+                  else torch.cuda.default_stream(t.device))
+    if stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    return torch.cuda.stream(stream)
+
+
+def _rows(t: torch.Tensor, name: str, dtype, device, shape) -> None:
+    """_need for a tensor of any strides whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 # --------------------------------------------------------------- host queries
@@ -344,6 +386,107 @@ def taylor_attn_state_merge(a, b, d_k: int, d_v: int, n: int, out=None, stream=N
     return out
 
 
+def _qk_args(q, k, freqs, positions, q_weight, k_weight, dtype):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k must be [B, N, H, d]")
+    B, N, Hq, d = q.shape
+    Hk = k.shape[2]
+    _rows(q, "q", dtype, q.device, q.shape)
+    _rows(k, "k", dtype, q.device, (B, N, Hk, d))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, torch.float32, q.device, (d,))
+    if positions is not None:
+        _need(positions, "positions", torch.int64, q.device, (B, N))
+    freqs = np.ascontiguousarray(freqs, dtype=np.float64)
+    if freqs.ndim != 1:
+        raise ValueError("freqs must hold one frequency for each rotated pair")
+    return B, N, Hq, Hk, d, freqs
+
+
+def _strides(t: torch.Tensor):
+    return (_I64 * 3)(*t.stride()[:3])
+
+
+def _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight, interleaved, eps, q_out, k_out,
+                  stream):
+    with _on(q, stream):
+        B, N, Hq, Hk, d, freqs = _qk_args(q, k, freqs, positions, q_weight, k_weight, dtype)
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, d), dtype=dtype, device=q.device)
+        else:
+            _need(q_out, "q_out", dtype, q.device, (B, Hq, N, d))
+        if k_out is None:
+            k_out = torch.empty((B, Hk, N, d), dtype=dtype, device=q.device)
+        else:
+            _need(k_out, "k_out", dtype, q.device, (B, Hk, N, d))
+        rc = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), int(pos0),
+                                  freqs.ctypes.data, 2 * len(freqs), int(bool(interleaved)), _ptr(q_out),
+                                  _ptr(k_out), B, N, Hq, Hk, d, _strides(q), _strides(k), float(eps), _stream(None))
+    _check(rc, name)
+    return q_out, k_out
+
+
+def taylor_attn_qk_norm_rope(q, k, freqs, positions=None, pos0: int = 0, q_weight=None, k_weight=None,
+                             interleaved: bool = False, eps: float = 0.0, q_out=None, k_out=None, stream=None):
+    """Unit norms and position rotation of bf16 q [B,N,Hq,d], k [B,N,Hk,d]
+    (any strides, last dimension contiguous) -> head-major q_out [B,Hq,N,d],
+    k_out [B,Hk,N,d].  ``freqs`` holds the rot/2 frequencies on the host
+    (rope_freqs); ``positions`` int64 [B,N], else pos0 + n."""
+    return _qk_norm_rope("taylor_attn_qk_norm_rope", torch.bfloat16, q, k, freqs, positions, pos0, q_weight,
+                         k_weight, interleaved, eps, q_out, k_out, stream)
+
+
+def taylor_attn_qk_norm_rope_f32(q, k, freqs, positions=None, pos0: int = 0, q_weight=None, k_weight=None,
+                                 interleaved: bool = False, eps: float = 0.0, q_out=None, k_out=None, stream=None):
+    """taylor_attn_qk_norm_rope with fp32 tensors."""
+    return _qk_norm_rope("taylor_attn_qk_norm_rope_f32", torch.float32, q, k, freqs, positions, pos0, q_weight,
+                         k_weight, interleaved, eps, q_out, k_out, stream)
+
+
+def _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, pos0, q_weight, k_weight,
+                           interleaved, eps, dq, dk, stream):
+    with _on(q, stream):
+        B, N, Hq, Hk, d, freqs = _qk_args(q, k, freqs, positions, q_weight, k_weight, dtype)
+        _need(dq_out, "dq_out", dtype, q.device, (B, Hq, N, d))
+        _need(dk_out, "dk_out", dtype, q.device, (B, Hk, N, d))
+        if dq is None:
+            dq = torch.empty((B, N, Hq, d), dtype=dtype, device=q.device)
+        else:
+            _rows(dq, "dq", dtype, q.device, q.shape)
+        if dk is None:
+            dk = torch.empty((B, N, Hk, d), dtype=dtype, device=q.device)
+        else:
+            _rows(dk, "dk", dtype, q.device, k.shape)
+        dqw = None if q_weight is None else torch.empty_like(q_weight)
+        dkw = None if k_weight is None else torch.empty_like(k_weight)
+        rc = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight), _ptr(k_weight),
+                                  _ptr(positions), int(pos0), freqs.ctypes.data, 2 * len(freqs),
+                                  int(bool(interleaved)), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), B, N, Hq, Hk, d,
+                                  _strides(q), _strides(k), _strides(dq), _strides(dk), float(eps), _stream(None))
+    _check(rc, name)
+    return dq, dk, dqw, dkw
+
+
+def taylor_attn_qk_norm_rope_backward(q, k, dq_out, dk_out, freqs, positions=None, pos0: int = 0, q_weight=None,
+                                      k_weight=None, interleaved: bool = False, eps: float = 0.0, dq=None, dk=None,
+                                      stream=None):
+    """Gradients (dq [B,N,Hq,d], dk [B,N,Hk,d], dq_weight, dk_weight) of
+    taylor_attn_qk_norm_rope from its inputs and dq_out [B,Hq,N,d], dk_out
+    [B,Hk,N,d]; ``dq``, ``dk`` may be slices of a packed gradient.  A weight's
+    gradient is None where there is no weight."""
+    return _qk_norm_rope_backward("taylor_attn_qk_norm_rope_backward", torch.bfloat16, q, k, dq_out, dk_out, freqs,
+                                  positions, pos0, q_weight, k_weight, interleaved, eps, dq, dk, stream)
+
+
+def taylor_attn_qk_norm_rope_backward_f32(q, k, dq_out, dk_out, freqs, positions=None, pos0: int = 0, q_weight=None,
+                                          k_weight=None, interleaved: bool = False, eps: float = 0.0, dq=None,
+                                          dk=None, stream=None):
+    """taylor_attn_qk_norm_rope_backward with fp32 tensors."""
+    return _qk_norm_rope_backward("taylor_attn_qk_norm_rope_backward_f32", torch.float32, q, k, dq_out, dk_out,
+                                  freqs, positions, pos0, q_weight, k_weight, interleaved, eps, dq, dk, stream)
+
+
 def taylor_attn_release_workspace() -> None:
     _check(lib().taylor_attn_release_workspace(), "taylor_attn_release_workspace")
 
@@ -385,6 +528,11 @@ def taylor_attn_timing_read(max_kernels: int = 16):
 
 
 # --------------------------------------------------------------- layout helpers
+
+def rope_freqs(rot: int, base: float = 10000.0) -> np.ndarray:
+    """The rot/2 frequencies base^(-2j/rot) of a rotation, float64 on the host."""
+    return float(base) ** (-np.arange(0, rot, 2) / max(rot, 1))
+
 
 def state_view(state: torch.Tensor, d_k: int, d_v: int, n: int):
     """Views (S_v [..., F, d_v], z [..., F]) into a flat state [..., stride]."""
