@@ -24,6 +24,7 @@
 #include "common.cuh"
 #include "entry.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace ta {
 
@@ -61,37 +62,27 @@ __device__ __forceinline__ float2 cos_sin(const QkArgs& a, int64_t p, int j) {
     return make_float2(c, s);
 }
 
-template <int G>
-__device__ __forceinline__ float group_sum(float v) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-template <int G>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// 1 / sqrt(sum x^2 + eps) over a group of G lanes.  Where the sum of squares
-// leaves fp32's comfortable range, x is first divided by its largest entry m,
-// and the result belongs to x / m (m is returned, else 1).  A row of zeros
-// with eps 0 gives 0: its output and its gradient are zero.  All 32 lanes
-// call it together.
-template <int G, int E>
-__device__ __forceinline__ float inv_norm(float (&x)[E], float eps, float& m) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(x[e], x[e], s);
-    s = group_sum<G>(s);
+// 1 / sqrt(sum x^2 + eps) of rows held by groups of `lanes` neighbouring lanes,
+// from a lane's entries x and the group's sum of squares s.  Where s leaves
+// fp32's comfortable range, x is first divided by its largest entry m, and the
+// result belongs to x / m (m is returned, else 1).  A row of zeros with eps 0
+// gives 0: its output and its gradient are zero.  All 32 lanes call it
+// together.
+template <int E>
+__device__ __forceinline__ float far_norm(float (&x)[E], float s, float eps, float& m, int lanes) {
     m = 1.f;
     const bool far = !(s > 1e-30f && s < 1e37f);
     if (__any_sync(0xffffffffu, far)) {
         float big = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(x[e]));
-        big = group_max<G>(big);
+        for (int o = lanes >> 1; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
         if (far && s == s && big > 0.f && big < INFINITY) m = big;
         float s2 = 0.f;
 #pragma unroll
@@ -99,8 +90,9 @@ __device__ __forceinline__ float inv_norm(float (&x)[E], float eps, float& m) {
             if (m != 1.f) x[e] /= m;
             s2 = fmaf(x[e], x[e], s2);
         }
-        s = group_sum<G>(s2) + (m != 1.f && eps > 0.f ? eps / m / m : eps);
-        return s == 0.f ? 0.f : rsqrtf(s);
+        for (int o = lanes >> 1; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+        s = s2 + (m != 1.f && eps > 0.f ? eps / m / m : eps);
+        return s != 0.f ? rsqrtf(s) : 0.f;
     }
     return rsqrtf(s + eps);
 }
@@ -146,7 +138,7 @@ qk_any_kernel(const __grid_constant__ QkArgs a, int slices) {
                 float x[2] = {lane < a.d ? to_float(xr[lane]) : 0.f,
                               lane + 32 < a.d ? to_float(xr[lane + 32]) : 0.f};
                 float m;
-                const float inv = inv_norm<32>(x, a.eps, m);
+                const float inv = far_norm<2>(x, warp_sum(fmaf(x[0], x[0], x[1] * x[1])), a.eps, m, 32);
                 float in[2];
                 if (BWD) {
                     const T* gr = static_cast<const T*>(a.dy[z]) + dense;
@@ -169,7 +161,7 @@ qk_any_kernel(const __grid_constant__ QkArgs a, int slices) {
                     acc[z][0] = fmaf(out[0], xh0, acc[z][0]);
                     acc[z][1] = fmaf(out[1], xh1, acc[z][1]);
                     const float g0 = out[0] * w0, g1 = out[1] * w1;
-                    const float along = group_sum<32>(g0 * xh0 + g1 * xh1);
+                    const float along = warp_sum(g0 * xh0 + g1 * xh1);
                     T* o = static_cast<T*>(a.y[z]) + b * a.ys[z][0] + n * a.ys[z][1] + h * a.ys[z][2];
                     out[0] = (g0 - xh0 * along) * inv;
                     out[1] = (g1 - xh1 * along) * inv;
@@ -199,6 +191,385 @@ qk_any_kernel(const __grid_constant__ QkArgs a, int slices) {
     }
 }
 
+// A row's piece of VE entries as it lies in memory: 4, 8 or 16 bytes.
+template <int W>
+struct __align__(4 * W) Piece {
+    uint32_t w[W];
+};
+// Asynchronous copy of one piece into shared memory.
+template <int W>
+__device__ __forceinline__ void fetch_piece(Piece<W>* dst, const void* src) {
+    if constexpr (W == 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(4 * W)
+                     : "memory");
+}
+template <int W>
+__device__ __forceinline__ void store_piece(void* p, const Piece<W>& r) {
+    if constexpr (W == 4) *static_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else if constexpr (W == 2) *static_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+    else *static_cast<unsigned int*>(p) = r.w[0];
+}
+// Two fp32 in a register pair: sm_100 multiplies and adds both in one
+// instruction, which this issue-bound kernel lives on.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 make2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split2(f32x2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float total2(f32x2 v) {
+    const float2 f = split2(v);
+    return f.x + f.y;
+}
+__device__ __forceinline__ f32x2 swap2(f32x2 v) {
+    const float2 f = split2(v);
+    return make2(f.y, f.x);
+}
+
+template <typename T, int VE>
+__device__ __forceinline__ void unpack(const Piece<VE * (int)sizeof(T) / 4>& r, f32x2 (&x)[VE / 2]) {
+#pragma unroll
+    for (int e = 0; e < VE / 2; ++e) {
+        if constexpr (sizeof(T) == 4) x[e] = make2(__uint_as_float(r.w[2 * e]), __uint_as_float(r.w[2 * e + 1]));
+        else x[e] = make2(__uint_as_float(r.w[e] << 16), __uint_as_float(r.w[e] & 0xffff0000u));
+    }
+}
+template <typename T, int VE>
+__device__ __forceinline__ Piece<VE * (int)sizeof(T) / 4> pack(const f32x2 (&x)[VE / 2]) {
+    Piece<VE * (int)sizeof(T) / 4> r;
+#pragma unroll
+    for (int e = 0; e < VE / 2; ++e) {
+        const float2 f = split2(x[e]);
+        if constexpr (sizeof(T) == 4) {
+            r.w[2 * e] = __float_as_uint(f.x);
+            r.w[2 * e + 1] = __float_as_uint(f.y);
+        } else {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f.x, f.y);
+            r.w[e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+    }
+    return r;
+}
+
+// v summed over groups of `lanes` neighbouring lanes, which LPR states where
+// it is not 0.
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v, int lanes) {
+    if constexpr (LPR > 0) {
+#pragma unroll
+        for (int o = LPR >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    } else {
+        for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
+}
+
+// Where a row's sum of squares s leaves fp32's comfortable range, scales the
+// row by a power of two to a largest entry in [1, 2) (exactly, but for entries
+// that are nothing beside it); the returned norm is that of the scaled row.  A
+// row of zeros with eps 0 has the norm's inverse 0, one with infinities or NaN
+// is left as it is.  Out of line: rows of ordinary size never come here.
+template <int W>
+struct Rescaled {
+    Piece<W> row;
+    float inv;
+    int by;  // the row was multiplied by 2^-by
+};
+template <typename T, int VE>
+__device__ __noinline__ Rescaled<VE * (int)sizeof(T) / 4> rescale(Piece<VE * (int)sizeof(T) / 4> r, float s, float eps,
+                                                                  int lanes) {
+    f32x2 x[VE / 2];
+    unpack<T, VE>(r, x);
+    float big = 0.f;
+#pragma unroll
+    for (int e = 0; e < VE / 2; ++e) {
+        const float2 f = split2(x[e]);
+        big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    const bool far = !(s > 1e-30f && s < 1e37f) && s == s && big > 0.f && big < INFINITY;
+    const int by = far ? ilogbf(big) : 0;
+    float s2 = 0.f;
+#pragma unroll
+    for (int e = 0; e < VE / 2; ++e) {
+        float2 f = split2(x[e]);
+        f.x = ldexpf(f.x, -by);
+        f.y = ldexpf(f.y, -by);
+        s2 += f.x * f.x + f.y * f.y;
+        x[e] = make2(f.x, f.y);
+    }
+    for (int o = lanes >> 1; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+    if (far) {
+        r = pack<T, VE>(x);
+        s = s2;
+        eps = ldexpf(eps, -2 * by);
+    }
+    s += eps;
+    return {r, s == 0.f ? 0.f : rsqrtf(s), by};
+}
+
+constexpr int kDepth = 4;  // pieces a thread has in flight: four rows forward, two backward (x and dy)
+constexpr int kCtas = 4;   // CTAs an SM holds, forward: 64 registers
+constexpr int kBackCtas = 3;
+
+// Rows in pieces of VE entries.  A row is held by `lpr` neighbouring lanes
+// (a power of two, one piece each; lanes past the row hold nothing), a CTA
+// takes `tok` tokens x `slices` head slices.  The tokens' angles are formed
+// once per CTA in shared memory; a thread keeps one token's and one piece's
+// cosines and sines (times the weights) in registers and walks its heads,
+// q's and then k's.  Its pieces arrive by asynchronous copies into a ring of
+// its own in shared memory, so that the bytes in flight cost no registers and
+// the first ones travel while the angles are formed.  The other entry of a
+// pair is in another lane's piece, exchanged as it was loaded.  Sums over a
+// row's lanes go through shuffles, all lanes of a warp together.
+//
+// Bytes bound the operator (about 10 to 14 operations a value), instructions
+// this kernel: at 8 bf16 a lane the 44 B a nanosecond and SM of the memory
+// leave some 180 issue slots a row and lane.  Four rows held in registers at
+// two CTAs an SM ran 113 us (B4 N8192, 16 + 16 heads of 64, bf16, forward,
+// 268 MB); the ring at four CTAs 79 us, 79 % of the issue slots taken; pairs
+// in f32x2 instructions, row pointers that step and lane counts known at
+// compile time 58 us, 4.6 TB/s.  Backward 84 us without weights, 101 us with
+// (403 MB); at 4 CTAs it spills (152 us), at 2 it waits (109 us).  Ring depths
+// of 4 and 8 are within 2 %.
+template <typename T, int VE, int LPR, bool BWD>
+__global__ void __launch_bounds__(256, BWD ? kBackCtas : kCtas)
+qk_vec_kernel(const __grid_constant__ QkArgs a, int lpr, int tok, int slices, int tiles) {
+    constexpr int W = VE * (int)sizeof(T) / 4, P = VE / 2;
+    constexpr int D = BWD ? kDepth / 2 : kDepth;  // rows in flight
+    __shared__ Piece<W> ring[kDepth][256];
+    __shared__ __align__(16) float cs[2][128 * VE];  // cos, sin: tok * rot / 2 <= 256 / lpr * VE * lpr / 2
+    __shared__ __align__(16) float ws[2][kMaxDk];    // weights of q and k, 1 without
+    __shared__ __align__(16) float dw[BWD ? 2 : 1][BWD ? 256 : 1][VE];  // this thread's share of the weights' gradients
+    if (LPR > 0) lpr = LPR;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int half = a.rot >> 1;
+    const int c = tid & (lpr - 1), tl = tid / lpr % tok, slice = tid / (lpr * tok);
+    const int hc = half / VE;  // pieces of half a rotation
+    const bool moved = !a.inter && c < 2 * hc;
+    const int mate = (lane & ~(lpr - 1)) + (moved ? (c < hc ? c + hc : c - hc) : c);
+    const unsigned tokens = (unsigned)a.B * (unsigned)a.N;
+    // rows of a thread in q and in both
+    const int rq = (a.H[0] + slices - 1) / slices, rows = rq + (a.H[1] + slices - 1) / slices;
+    for (int i = tid; i < 2 * kMaxDk; i += 256) {
+        const int z = i / kMaxDk, e = i % kMaxDk;
+        ws[z][e] = a.w[z] && e < a.d ? a.w[z][e] : 1.f;
+    }
+    if (BWD) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) dw[0][tid][e] = dw[1][tid][e] = 0.f;
+    }
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const unsigned t0 = (unsigned)tile * (unsigned)tok, t = t0 + tl;
+        const bool live = t < tokens && c * VE < a.d;
+        const int b = live ? t / (unsigned)a.N : 0, n = live ? t - (unsigned)b * (unsigned)a.N : 0;
+        const T* xk = static_cast<const T*>(a.x[1]) + b * a.xs[1][0] + n * a.xs[1][1] + slice * a.xs[1][2] + c * VE;
+        const T* xr = static_cast<const T*>(a.x[0]) + b * a.xs[0][0] + n * a.xs[0][1] + slice * a.xs[0][2] + c * VE;
+        int64_t xstep = slices * a.xs[0][2];
+        // rows of the dense head-major tensors: dy, or the output
+        const int64_t dense = (int64_t)a.N * a.d, gstep = slices * dense;
+        const int64_t at[2] = {((int64_t)b * a.H[0] + slice) * dense + (int64_t)n * a.d + c * VE,
+                               ((int64_t)b * a.H[1] + slice) * dense + (int64_t)n * a.d + c * VE};
+        const T* gr = BWD ? static_cast<const T*>(a.dy[0]) + at[0] : nullptr;
+        int fr = 0, fh = slice, fH = a.H[0];  // the next row to fetch, its head
+        if (rq == 0) xr = xk, xstep = slices * a.xs[1][2], fH = a.H[1], gr = static_cast<const T*>(a.dy[1]) + at[1];
+        auto fetch = [&]() {
+            if (fr < rows) {
+                if (live && fh < fH) {
+                    fetch_piece<W>(&ring[fr % D][tid], xr);
+                    if (BWD) fetch_piece<W>(&ring[D + fr % D][tid], gr);
+                }
+                ++fr;
+                fh += slices;
+                xr += xstep;
+                if (BWD) gr += gstep;
+                if (fr == rq) {
+                    xr = xk, xstep = slices * a.xs[1][2];
+                    fh = slice, fH = a.H[1];
+                    if (BWD) gr = static_cast<const T*>(a.dy[1]) + at[1];
+                }
+            }
+            ptx::cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < D; ++i) fetch();
+        if (half > 0) {
+            int hp = 1;  // lanes of one token's frequencies
+            while (hp < half) hp *= 2;
+            const int j = tid & (hp - 1);
+            const unsigned n0 = t0 % (unsigned)a.N;
+            for (int ti = tid / hp; ti < tok; ti += 256 / hp) {
+                const unsigned ta = t0 + ti, na = n0 + ti;
+                if (j < half && ta < tokens) {
+                    const float2 v = cos_sin(a, a.pos ? a.pos[ta] : a.pos0 + (na < a.N ? na : na % (unsigned)a.N), j);
+                    cs[0][ti * half + j] = v.x;
+                    cs[1][ti * half + j] = v.y;
+                }
+            }
+        }
+        __syncthreads();
+        int r = 0;
+#pragma unroll 1
+        for (int z = 0; z < 2; ++z) {
+            f32x2 C[P], S[P], acc[P] = {};
+            const f32x2* wc = reinterpret_cast<const f32x2*>(&ws[z][c * VE]);
+            if (!a.inter) {
+                // the pair's frequencies and the partner's weights lie as the entries do
+                const int m = moved ? (c < hc ? c + hc : c - hc) : c;
+                const int j = tl * half + (moved ? (c < hc ? c : c - hc) * VE : 0);
+                const f32x2* wm = reinterpret_cast<const f32x2*>(&ws[z][m * VE]);
+                const float sign = (c < hc) != BWD ? -1.f : 1.f;
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    C[e] = moved ? reinterpret_cast<const f32x2*>(&cs[0][j])[e] : make2(1.f, 1.f);
+                    S[e] = moved ? mul2(reinterpret_cast<const f32x2*>(&cs[1][j])[e], make2(sign, sign)) : 0;
+                    if (!BWD) C[e] = mul2(C[e], wc[e]), S[e] = mul2(S[e], wm[e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const int i = c * VE + 2 * e;
+                    const bool in = i < a.rot;
+                    const float co = in ? cs[0][tl * half + i / 2] : 1.f, si = in ? cs[1][tl * half + i / 2] : 0.f;
+                    C[e] = make2(co, co);
+                    S[e] = BWD ? make2(si, -si) : make2(-si, si);
+                    if (!BWD) C[e] = mul2(C[e], wc[e]), S[e] = mul2(S[e], swap2(wc[e]));
+                }
+            }
+            T* y = BWD ? static_cast<T*>(a.y[z]) + b * a.ys[z][0] + n * a.ys[z][1] + slice * a.ys[z][2] + c * VE
+                       : static_cast<T*>(a.y[z]) + at[z];
+            const int64_t ystep = BWD ? slices * a.ys[z][2] : gstep;
+            const int end = z ? rows : rq;
+#pragma unroll 1
+            for (int h = slice; r < end; ++r, h += slices, y += ystep) {
+                const bool on = live && h < a.H[z];
+                ptx::cp_async_wait<D - 1>();
+                Piece<W> px = {}, pg = {};
+                if (on) {
+                    px = ring[r % D][tid];
+                    if (BWD) pg = ring[D + r % D][tid];
+                }
+                fetch();
+                f32x2 x[P];
+                unpack<T, VE>(px, x);
+                f32x2 sq = mul2(x[0], x[0]);
+#pragma unroll
+                for (int e = 1; e < P; ++e) sq = fma2(x[e], x[e], sq);
+                const float s = row_sum<LPR>(total2(sq), lpr);
+                float inv;
+                asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(on ? s + a.eps : 1.f));
+                int by = 0;
+                const bool any = __any_sync(0xffffffffu, on && !(s > 1e-30f && s < 1e37f));
+                if (any) {
+                    const Rescaled<W> q = rescale<T, VE>(px, s, a.eps, lpr);
+                    if (on) px = q.row, inv = q.inv, by = q.by;
+                    unpack<T, VE>(px, x);
+                }
+                const f32x2 inv2 = make2(inv, inv);
+                const Piece<W>& mine = BWD ? pg : px;
+                f32x2 in[P], other[P], out[P];
+                unpack<T, VE>(mine, in);
+                if (a.inter) {
+#pragma unroll
+                    for (int e = 0; e < P; ++e) other[e] = swap2(in[e]);
+                } else {
+                    Piece<W> far;
+#pragma unroll
+                    for (int i = 0; i < W; ++i) far.w[i] = __shfl_sync(0xffffffffu, mine.w[i], mate);
+                    unpack<T, VE>(far, other);
+                }
+                if (BWD) {
+                    f32x2 sum = 0;
+#pragma unroll
+                    for (int e = 0; e < P; ++e) {
+                        out[e] = fma2(other[e], S[e], mul2(in[e], C[e]));  // du
+                        x[e] = mul2(x[e], inv2);                           // xhat
+                    }
+                    if (a.w[z]) {
+#pragma unroll
+                        for (int e = 0; e < P; ++e) {
+                            acc[e] = fma2(out[e], x[e], acc[e]);
+                            out[e] = mul2(out[e], wc[e]);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < P; ++e) sum = fma2(out[e], x[e], sum);  // g . xhat
+                    const float along = -row_sum<LPR>(total2(sum), lpr);
+                    const f32x2 along2 = make2(along, along);
+#pragma unroll
+                    for (int e = 0; e < P; ++e) out[e] = mul2(fma2(x[e], along2, out[e]), inv2);
+                    if (any) {
+#pragma unroll
+                        for (int e = 0; e < P; ++e) {
+                            const float2 f = split2(out[e]);
+                            out[e] = make2(ldexpf(f.x, -by), ldexpf(f.y, -by));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < P; ++e) out[e] = mul2(fma2(other[e], S[e], mul2(in[e], C[e])), inv2);
+                }
+                if (on) store_piece<W>(y, pack<T, VE>(out));
+            }
+            if (BWD && a.w[z]) {
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    const float2 f = split2(acc[e]);
+                    dw[z][tid][2 * e] += f.x;
+                    dw[z][tid][2 * e + 1] += f.y;
+                }
+            }
+        }
+        __syncthreads();  // cs is free for the next tile
+    }
+    if (BWD && a.dw) {  // the last barrier above stands between the sums and their readers
+        for (int i = tid; i < 2 * a.d; i += 256) {
+            const int z = i / a.d, e = i - z * a.d;
+            float v = 0.f;
+            for (int g = e / VE; g < 256; g += lpr) v += dw[z][g][e % VE];
+            a.dw[(int64_t)blockIdx.x * 2 * a.d + i] = v;
+        }
+    }
+}
+
+template <typename T, bool BWD>
+using QkKernel = void (*)(QkArgs, int, int, int, int);
+
+// 16-byte pieces with the row's lanes known at compile time, narrower ones
+// (rows of odd lengths or alignment) with the count at run time.
+template <typename T, bool BWD>
+QkKernel<T, BWD> qk_vec(int ve, int lpr) {
+    constexpr int full = 16 / (int)sizeof(T);
+    if (ve == full) {
+        switch (lpr) {
+            case 1: return qk_vec_kernel<T, full, 1, BWD>;
+            case 2: return qk_vec_kernel<T, full, 2, BWD>;
+            case 4: return qk_vec_kernel<T, full, 4, BWD>;
+            case 8: return qk_vec_kernel<T, full, 8, BWD>;
+            default: return qk_vec_kernel<T, full, 64 / full, BWD>;
+        }
+    }
+    if (ve == 4) return qk_vec_kernel<T, 4, 0, BWD>;
+    return qk_vec_kernel<T, 2, 0, BWD>;
+}
+
 // dw[z][c] = sum of the CTAs' partials, one warp per column, in a fixed order.
 __global__ void __launch_bounds__(256)
 qk_weight_grad_kernel(const float* __restrict__ part, int parts, int d, float* dqw, float* dkw) {
@@ -206,37 +577,90 @@ qk_weight_grad_kernel(const float* __restrict__ part, int parts, int d, float* d
     if (col >= 2 * d) return;
     float v = 0.f;
     for (int i = lane; i < parts; i += 32) v += part[(int64_t)i * 2 * d + col];
-    v = group_sum<32>(v);
+    v = warp_sum(v);
     float* out = col < d ? dqw : dkw;
     if (lane == 0 && out) out[col < d ? col : col - d] = v;
 }
 
+// Whether the rows can be moved in pieces of VE entries: their length, the
+// distance between the two entries of a pair, and every address.
 template <typename T, bool BWD>
-cudaError_t launch_qk(QkArgs& a, float* dqw, float* dkw, cudaStream_t stream) {
+bool in_pieces(const QkArgs& a, int VE) {
+    const size_t bytes = VE * sizeof(T);
+    if (a.d % VE != 0 || (!a.inter && (a.rot / 2) % VE != 0)) return false;
+    for (int z = 0; z < 2; ++z) {
+        if (a.H[z] == 0) continue;
+        if (!entry::aligned(a.x[z], bytes) || !entry::aligned(a.y[z], bytes)) return false;
+        if (BWD && !entry::aligned(a.dy[z], bytes)) return false;
+        for (int i = 0; i < 3; ++i)
+            if (a.xs[z][i] % VE != 0 || (BWD && a.ys[z][i] % VE != 0)) return false;
+    }
+    return true;
+}
+
+struct QkPlan {
+    int ve, lpr, tok, slices;
+    int64_t grid;
+};
+
+template <typename T, bool BWD>
+QkPlan plan_qk(const QkArgs& a, bool weights) {
     const int sms = entry::num_sms();
     const int64_t tokens = (int64_t)a.B * a.N;
     const int heads = a.H[0] > a.H[1] ? a.H[0] : a.H[1];
-    // enough warps to fill the GPU before a warp takes several heads
-    int slices = 1;
-    while (slices < heads && tokens * slices < (int64_t)sms * 32) slices *= 2;
-    if (slices > heads) slices = heads;
-    int64_t grid = (tokens * slices + 7) / 8;
-    if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
-    float* part = nullptr;
-    if (BWD && (dqw || dkw)) {
-        const cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&part), (size_t)grid * 2 * a.d * 4, stream);
+    QkPlan p = {};
+    for (int ve = 16 / (int)sizeof(T); ve >= 2 && !p.ve; ve /= 2)
+        if (in_pieces<T, BWD>(a, ve)) p.ve = ve;
+    if (!p.ve) {
+        // enough warps to fill the GPU before a warp takes several heads
+        p.slices = 1;
+        while (p.slices < heads && tokens * p.slices < (int64_t)sms * 32) p.slices *= 2;
+        if (p.slices > heads) p.slices = heads;
+        p.grid = (tokens * p.slices + 7) / 8;
+        if (p.grid > (int64_t)sms * 8) p.grid = (int64_t)sms * 8;
+        return p;
+    }
+    p.lpr = 1;
+    while (p.lpr * p.ve < a.d) p.lpr *= 2;
+    // a thread walks all heads of a token where that fills the GPU (the more
+    // heads, the less the angles cost: 58 us at one slice, 62 us at two, 73 us
+    // at four on 32,768 tokens of 16 + 16 heads), else a slice of them, up to
+    // one wave of CTAs
+    p.slices = 1;
+    while (p.slices * p.lpr < 256 && p.slices < heads && tokens * p.lpr * p.slices * 2 <= (int64_t)sms * kCtas * 256)
+        p.slices *= 2;
+    p.tok = 256 / (p.lpr * p.slices);
+    p.grid = (tokens + p.tok - 1) / p.tok;
+    // with weight gradients, as many CTAs as fit at once: fewer partial sums
+    // to join
+    if (weights && p.grid > (int64_t)sms * kBackCtas) p.grid = (int64_t)sms * kBackCtas;
+    return p;
+}
+
+template <typename T, bool BWD>
+cudaError_t launch_qk(QkArgs& a, float* dqw, float* dkw, cudaStream_t stream) {
+    const bool weights = BWD && (dqw || dkw);
+    const QkPlan p = plan_qk<T, BWD>(a, weights);
+    const unsigned grid = (unsigned)p.grid;
+    if (weights) {
+        const cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&a.dw), (size_t)grid * 2 * a.d * 4, stream);
         if (e != cudaSuccess) return e;
     }
-    a.dw = part;
-    TA_TIMED(stream, "qk_any_kernel", qk_any_kernel<T, BWD><<<(unsigned)grid, 256, 0, stream>>>(a, slices));
+    if (!p.ve) {
+        TA_TIMED(stream, "qk_any_kernel", qk_any_kernel<T, BWD><<<grid, 256, 0, stream>>>(a, p.slices));
+    } else {
+        const int tiles = (int)(((int64_t)a.B * a.N + p.tok - 1) / p.tok);
+        const QkKernel<T, BWD> kernel = qk_vec<T, BWD>(p.ve, p.lpr);
+        TA_TIMED(stream, "qk_vec_kernel", kernel<<<grid, 256, 0, stream>>>(a, p.lpr, p.tok, p.slices, tiles));
+    }
     cudaError_t e = cudaGetLastError();
-    if (part) {
+    if (weights) {
         if (e == cudaSuccess) {
             TA_TIMED(stream, "qk_weight_grad_kernel",
-                     qk_weight_grad_kernel<<<(2 * a.d + 7) / 8, 256, 0, stream>>>(part, (int)grid, a.d, dqw, dkw));
+                     qk_weight_grad_kernel<<<(2 * a.d + 7) / 8, 256, 0, stream>>>(a.dw, (int)grid, a.d, dqw, dkw));
             e = cudaGetLastError();
         }
-        const cudaError_t f = workspace_free(part, stream);
+        const cudaError_t f = workspace_free(a.dw, stream);
         if (e == cudaSuccess) e = f;
     }
     return e;
