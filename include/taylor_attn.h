@@ -280,6 +280,70 @@ TAYLOR_API int taylor_attn_qk_norm_rope_backward_f32(const float* q, const float
                                                      const int64_t* k_strides, const int64_t* dq_strides,
                                                      const int64_t* dk_strides, float eps, cudaStream_t stream);
 
+/* Gated linear recurrence over a sequence, channel by channel: with
+ * a_t = sigmoid(gate_t),
+ *     h_t = a_t h_{t-1} + (1 - a_t) x_t      (coupled != 0)
+ *     h_t = a_t h_{t-1} + x_t                (coupled == 0).
+ * Like the attention's, its state has a fixed size; it is carried in fp32.
+ * gate, x [B][N][D] bf16 (the _f32 variant: fp32) with the strides
+ * gate_strides, x_strides: HOST arrays of two (batch, token) in elements,
+ * >= 0, the D channels contiguous; halves of one projection's rows are such.
+ * h0 fp32 [B][D] is the state before the first token, or NULL (zero).  h
+ * [B][N][D] is dense, of gate's type, and must not overlap the inputs; h_last
+ * fp32 [B][D] (may be NULL, may be h0) receives the state after the last
+ * token, unrounded, from which a later call or taylor_attn_gated_step
+ * continues.  lengths int32 [B] on the device, or NULL: sequence b has
+ * lengths[b] tokens (taken into 0..N); rows past them are not read, their h is
+ * written as zero, and h_last is the state after the sequence's own last
+ * token.  A gate of -inf resets the state (a is below 2^-125).  Pointers need
+ * the alignment of their elements only; with D, strides and pointers that
+ * allow it, four channels move at a time.  B*N, B*D < 2^31.  No workspace. */
+TAYLOR_API int taylor_attn_gated_scan(const void* gate, const void* x, const float* h0, const int32_t* lengths,
+                                      void* h, float* h_last, int B, int N, int D, const int64_t* gate_strides,
+                                      const int64_t* x_strides, int coupled, cudaStream_t stream);
+
+/* taylor_attn_gated_scan with fp32 gate, x and h. */
+TAYLOR_API int taylor_attn_gated_scan_f32(const float* gate, const float* x, const float* h0,
+                                          const int32_t* lengths, float* h, float* h_last, int B, int N, int D,
+                                          const int64_t* gate_strides, const int64_t* x_strides, int coupled,
+                                          cudaStream_t stream);
+
+/* Gradient of taylor_attn_gated_scan: from its inputs, its output h and the
+ * gradients dh [B][N][D] (dense) of h and dh_last fp32 [B][D] (NULL: zero) of
+ * the last state,
+ *     G_t = dh_t + a_{t+1} G_{t+1},  dx_t = G_t (1 - a_t | 1),
+ *     dgate_t = G_t (h_{t-1} - x_t | h_{t-1}) a_t (1 - a_t),  dh0 = a_0 G_0,
+ * into dgate, dx (strides dgate_strides, dx_strides as above, every element at
+ * its own address) and dh0 fp32 [B][D] (may be NULL, may be dh_last).  h_{t-1}
+ * is the stored h, as rounded.  Rows past a length have zero gradients. */
+TAYLOR_API int taylor_attn_gated_scan_backward(const void* gate, const void* x, const void* h, const void* dh,
+                                               const float* h0, const int32_t* lengths, const float* dh_last,
+                                               void* dgate, void* dx, float* dh0, int B, int N, int D,
+                                               const int64_t* gate_strides, const int64_t* x_strides,
+                                               const int64_t* dgate_strides, const int64_t* dx_strides, int coupled,
+                                               cudaStream_t stream);
+
+/* taylor_attn_gated_scan_backward with fp32 tensors. */
+TAYLOR_API int taylor_attn_gated_scan_backward_f32(const float* gate, const float* x, const float* h,
+                                                   const float* dh, const float* h0, const int32_t* lengths,
+                                                   const float* dh_last, float* dgate, float* dx, float* dh0, int B,
+                                                   int N, int D, const int64_t* gate_strides,
+                                                   const int64_t* x_strides, const int64_t* dgate_strides,
+                                                   const int64_t* dx_strides, int coupled, cudaStream_t stream);
+
+/* One token of the recurrence: gate, x [B][D] with the row strides
+ * gate_stride, x_stride (elements), state_in fp32 [B][D]; writes the new state
+ * to state_out (may be state_in) and, rounded to gate's type, to out [B][D]
+ * (dense).  No workspace. */
+TAYLOR_API int taylor_attn_gated_step(const void* gate, const void* x, const float* state_in, float* state_out,
+                                      void* out, int B, int D, int64_t gate_stride, int64_t x_stride, int coupled,
+                                      cudaStream_t stream);
+
+/* taylor_attn_gated_step with fp32 gate, x and out. */
+TAYLOR_API int taylor_attn_gated_step_f32(const float* gate, const float* x, const float* state_in,
+                                          float* state_out, float* out, int B, int D, int64_t gate_stride,
+                                          int64_t x_stride, int coupled, cudaStream_t stream);
+
 /* taylor_attn_prefill_f32 for callers that cannot allocate device memory
  * (a plugin whose host framework owns all device memory, a serving loop that
  * reserves memory up front and must not see an allocation fail mid-step).

@@ -58,6 +58,12 @@ SIGNATURES = {
         (_I, [_P, _P, _P, _P, *_QK, _P, _P, _P, _P, *_SIZES, _P, _P, _P, _P, _F, _P]),
     "taylor_attn_qk_norm_rope_backward_f32":
         (_I, [_P, _P, _P, _P, *_QK, _P, _P, _P, _P, *_SIZES, _P, _P, _P, _P, _F, _P]),
+    "taylor_attn_gated_scan": (_I, [*[_P] * 6, *[_I] * 3, _P, _P, _I, _P]),
+    "taylor_attn_gated_scan_f32": (_I, [*[_P] * 6, *[_I] * 3, _P, _P, _I, _P]),
+    "taylor_attn_gated_scan_backward": (_I, [*[_P] * 10, *[_I] * 3, *[_P] * 4, _I, _P]),
+    "taylor_attn_gated_scan_backward_f32": (_I, [*[_P] * 10, *[_I] * 3, *[_P] * 4, _I, _P]),
+    "taylor_attn_gated_step": (_I, [*[_P] * 5, _I, _I, _I64, _I64, _I, _P]),
+    "taylor_attn_gated_step_f32": (_I, [*[_P] * 5, _I, _I, _I64, _I64, _I, _P]),
     "taylor_attn_prefill_f32_noalloc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "taylor_attn_prefill_noalloc_scratch_floats": (_I64, []),
     "taylor_attn_device_errors": (_I, [_I, _P]),
@@ -485,6 +491,134 @@ def taylor_attn_qk_norm_rope_backward_f32(q, k, dq_out, dk_out, freqs, positions
     """taylor_attn_qk_norm_rope_backward with fp32 tensors."""
     return _qk_norm_rope_backward("taylor_attn_qk_norm_rope_backward_f32", torch.float32, q, k, dq_out, dk_out,
                                   freqs, positions, pos0, q_weight, k_weight, interleaved, eps, dq, dk, stream)
+
+
+def _gated_args(gate, x, h0, lengths, dtype):
+    if gate.dim() != 3:
+        raise ValueError("gate, x must be [B, N, D]")
+    B, N, D = gate.shape
+    _rows(gate, "gate", dtype, gate.device, gate.shape)
+    _rows(x, "x", dtype, gate.device, gate.shape)
+    if h0 is not None:
+        _need(h0, "h0", torch.float32, gate.device, (B, D))
+    if lengths is not None:
+        _need(lengths, "lengths", torch.int32, gate.device, (B,))
+    return B, N, D
+
+
+def _two(t: torch.Tensor):
+    return (_I64 * 2)(*t.stride()[:2])
+
+
+def _gated_scan(name, dtype, gate, x, coupled, h0, lengths, h, h_last, stream):
+    with _on(gate, stream):
+        B, N, D = _gated_args(gate, x, h0, lengths, dtype)
+        if h is None:
+            h = torch.empty((B, N, D), dtype=dtype, device=gate.device)
+        else:
+            _need(h, "h", dtype, gate.device, (B, N, D))
+        if h_last is True:
+            h_last = torch.empty((B, D), dtype=torch.float32, device=gate.device)
+        elif h_last is not None:
+            _need(h_last, "h_last", torch.float32, gate.device, (B, D))
+        rc = getattr(lib(), name)(_ptr(gate), _ptr(x), _ptr(h0), _ptr(lengths), _ptr(h), _ptr(h_last), B, N, D,
+                                  _two(gate), _two(x), int(bool(coupled)), _stream(None))
+    _check(rc, name)
+    return h, h_last
+
+
+def taylor_attn_gated_scan(gate, x, coupled: bool = True, h0=None, lengths=None, h=None, h_last=None, stream=None):
+    """Gated linear recurrence h_t = a_t h_{t-1} + (1 - a_t) x_t (without
+    ``coupled``: + x_t), a = sigmoid(gate), over bf16 gate, x [B,N,D] (any
+    strides, last dimension contiguous) -> (h [B,N,D], last state fp32 [B,D]
+    or None).  ``h_last=True`` has the last state allocated and returned; it
+    may also be ``h0``.  ``lengths`` int32 [B]: rows past them give zeros."""
+    return _gated_scan("taylor_attn_gated_scan", torch.bfloat16, gate, x, coupled, h0, lengths, h, h_last, stream)
+
+
+def taylor_attn_gated_scan_f32(gate, x, coupled: bool = True, h0=None, lengths=None, h=None, h_last=None,
+                               stream=None):
+    """taylor_attn_gated_scan with fp32 tensors."""
+    return _gated_scan("taylor_attn_gated_scan_f32", torch.float32, gate, x, coupled, h0, lengths, h, h_last, stream)
+
+
+def _gated_scan_backward(name, dtype, gate, x, h, dh, coupled, h0, lengths, dh_last, dgate, dx, dh0, stream):
+    with _on(gate, stream):
+        B, N, D = _gated_args(gate, x, h0, lengths, dtype)
+        _need(h, "h", dtype, gate.device, (B, N, D))
+        _need(dh, "dh", dtype, gate.device, (B, N, D))
+        if dh_last is not None:
+            _need(dh_last, "dh_last", torch.float32, gate.device, (B, D))
+        if dgate is None:
+            dgate = torch.empty((B, N, D), dtype=dtype, device=gate.device)
+        else:
+            _rows(dgate, "dgate", dtype, gate.device, (B, N, D))
+        if dx is None:
+            dx = torch.empty((B, N, D), dtype=dtype, device=gate.device)
+        else:
+            _rows(dx, "dx", dtype, gate.device, (B, N, D))
+        if dh0 is True:
+            dh0 = torch.empty((B, D), dtype=torch.float32, device=gate.device)
+        elif dh0 is False:
+            dh0 = None
+        elif dh0 is not None:
+            _need(dh0, "dh0", torch.float32, gate.device, (B, D))
+        rc = getattr(lib(), name)(_ptr(gate), _ptr(x), _ptr(h), _ptr(dh), _ptr(h0), _ptr(lengths), _ptr(dh_last),
+                                  _ptr(dgate), _ptr(dx), _ptr(dh0), B, N, D, _two(gate), _two(x), _two(dgate),
+                                  _two(dx), int(bool(coupled)), _stream(None))
+    _check(rc, name)
+    return dgate, dx, dh0
+
+
+def taylor_attn_gated_scan_backward(gate, x, h, dh, coupled: bool = True, h0=None, lengths=None, dh_last=None,
+                                    dgate=None, dx=None, dh0=None, stream=None):
+    """Gradients (dgate [B,N,D], dx [B,N,D], dh0 fp32 [B,D] or None) of
+    taylor_attn_gated_scan from its inputs, its output h and the gradients dh
+    [B,N,D], dh_last fp32 [B,D]; ``dgate``, ``dx`` may be slices of a packed
+    gradient; ``dh0=True`` has the first state's gradient allocated."""
+    return _gated_scan_backward("taylor_attn_gated_scan_backward", torch.bfloat16, gate, x, h, dh, coupled, h0,
+                                lengths, dh_last, dgate, dx, dh0, stream)
+
+
+def taylor_attn_gated_scan_backward_f32(gate, x, h, dh, coupled: bool = True, h0=None, lengths=None, dh_last=None,
+                                        dgate=None, dx=None, dh0=None, stream=None):
+    """taylor_attn_gated_scan_backward with fp32 tensors."""
+    return _gated_scan_backward("taylor_attn_gated_scan_backward_f32", torch.float32, gate, x, h, dh, coupled, h0,
+                                lengths, dh_last, dgate, dx, dh0, stream)
+
+
+def _gated_step(name, dtype, gate, x, state, coupled, out, state_out, stream):
+    with _on(gate, stream):
+        if gate.dim() != 2:
+            raise ValueError("gate, x must be [B, D]")
+        B, D = gate.shape
+        _rows(gate, "gate", dtype, gate.device, (B, D))
+        _rows(x, "x", dtype, gate.device, (B, D))
+        _need(state, "state", torch.float32, gate.device, (B, D))
+        if state_out is None:
+            state_out = state
+        else:
+            _need(state_out, "state_out", torch.float32, gate.device, (B, D))
+        if out is None:
+            out = torch.empty((B, D), dtype=dtype, device=gate.device)
+        else:
+            _need(out, "out", dtype, gate.device, (B, D))
+        rc = getattr(lib(), name)(_ptr(gate), _ptr(x), _ptr(state), _ptr(state_out), _ptr(out), B, D, gate.stride(0),
+                                  x.stride(0), int(bool(coupled)), _stream(None))
+    _check(rc, name)
+    return out
+
+
+def taylor_attn_gated_step(gate, x, state, coupled: bool = True, out=None, state_out=None, stream=None):
+    """One token of the gated recurrence: bf16 gate, x [B,D] (rows of any
+    stride), ``state`` fp32 [B,D] is updated in place unless ``state_out`` is
+    given; returns out [B,D], the new state rounded."""
+    return _gated_step("taylor_attn_gated_step", torch.bfloat16, gate, x, state, coupled, out, state_out, stream)
+
+
+def taylor_attn_gated_step_f32(gate, x, state, coupled: bool = True, out=None, state_out=None, stream=None):
+    """taylor_attn_gated_step with fp32 tensors."""
+    return _gated_step("taylor_attn_gated_step_f32", torch.float32, gate, x, state, coupled, out, state_out, stream)
 
 
 def taylor_attn_release_workspace() -> None:

@@ -72,3 +72,53 @@ def test_binding_refuses_cpu_tensors():
 def test_rope_freqs():
     np.testing.assert_allclose(TA.rope_freqs(4, 100.0), [1.0, 0.1])
     assert len(TA.rope_freqs(0)) == 0
+
+
+def _two(*v):
+    return (ctypes.c_int64 * 2)(*v)
+
+
+def _scan(backward=False, **over):
+    B, N, D = 2, 5, 8
+    a = dict(gate=P, x=P, h=P, dh=P, h0=None, lengths=None, dl=None, y=P, dgate=P, dx=P, end=None, B=B, N=N, D=D,
+             gs=_two(N * D, D), xs=_two(N * D, D), dgs=_two(N * D, D), dxs=_two(N * D, D))
+    a.update(over)
+    L = TA.lib()
+    if backward:
+        return L.taylor_attn_gated_scan_backward(a["gate"], a["x"], a["h"], a["dh"], a["h0"], a["lengths"], a["dl"],
+                                                 a["dgate"], a["dx"], a["end"], a["B"], a["N"], a["D"], a["gs"],
+                                                 a["xs"], a["dgs"], a["dxs"], 1, None)
+    return L.taylor_attn_gated_scan(a["gate"], a["x"], a["h0"], a["lengths"], a["y"], a["end"], a["B"], a["N"],
+                                    a["D"], a["gs"], a["xs"], 1, None)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("over,status", [
+    (dict(B=-1), INV), (dict(N=-1), INV), (dict(D=-1), INV), (dict(gate=None), INV), (dict(x=None), INV),
+    (dict(gs=None), INV), (dict(xs=_two(40, -8)), INV), (dict(gate=P + 1), MIS), (dict(h0=P + 2), MIS),
+    (dict(lengths=P + 1), MIS), (dict(end=P + 2), MIS), (dict(B=1 << 16, N=1 << 15), UNS),
+    (dict(B=1 << 16, D=1 << 15), UNS), (dict(B=0, gate=None), OK), (dict(D=0, x=None), OK),
+    (dict(N=0, gate=None, x=None), OK),
+])
+def test_gated_scan_refuses(backward, over, status):
+    assert _scan(backward, **over) == status
+
+
+def test_gated_scan_refuses_more():
+    assert _scan(y=None) == INV
+    for name in ("h", "dh", "dgate", "dx", "dgs", "dxs"):
+        assert _scan(True, **{name: None}) == INV, name
+    assert _scan(True, dgs=_two(0, 8)) == INV and _scan(True, dxs=_two(40, 4)) == INV
+    assert _scan(True, dx=P + 1) == MIS and _scan(True, dl=P + 1) == MIS
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(B=-1), INV), (dict(D=-1), INV), (dict(gs=-1), INV), (dict(gate=None), INV), (dict(out=None), INV),
+    (dict(state=None), INV), (dict(gate=P + 1), MIS), (dict(state=P + 2), MIS), (dict(B=0, gate=None), OK),
+    (dict(D=0, out=None), OK),
+])
+def test_gated_step_refuses(over, status):
+    a = dict(gate=P, x=P, state=P, out=P, B=2, D=8, gs=8, xs=8)
+    a.update(over)
+    assert TA.lib().taylor_attn_gated_step(a["gate"], a["x"], a["state"], a["state"], a["out"], a["B"], a["D"],
+                                           a["gs"], a["xs"], 1, None) == status
