@@ -31,14 +31,25 @@ struct ScanArgs {
     int B, N, D, coupled;
 };
 
-// a = sigmoid(g) and 1 - a.  The exponent is capped so that e a is finite: a
-// gate of -inf leaves a = 2^-126 of the state and 1 - a = 1.  NaN stays NaN.
+// a = sigmoid(g) and 1 - a.  The exponential is capped so that e a is finite:
+// a gate of -inf leaves a < 2^-125 of the state and 1 - a = 1.  NaN stays NaN.
+// Beside bf16 gates and outputs the hardware's approximate exponential and
+// reciprocal (2 and 1 steps off) do; with fp32 tensors a memory of hundreds of
+// tokens would show their errors, so exponential and division are full ones.
+template <typename T>
 __device__ __forceinline__ void gates(float g, float& a, float& keep) {
-    float t = g * -1.4426950408889634f;
-    asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(t));  // 126
     float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(1.0f + e));
+    if constexpr (sizeof(T) == 2) {
+        float t = g * -1.4426950408889634f;
+        asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(t));  // 126
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(1.0f + e));
+    } else {
+        float t = -g;
+        asm("min.NaN.f32 %0, %0, 0f42AE0000;" : "+f"(t));  // 87
+        e = expf(t);
+        a = __frcp_rn(1.0f + e);
+    }
     keep = e * a;
 }
 
@@ -49,69 +60,312 @@ __device__ __forceinline__ float round_to<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// One thread per channel, token by token.
-template <typename T>
-__global__ void __launch_bounds__(128) scan_channel_kernel(const __grid_constant__ ScanArgs a) {
-    const int d = blockIdx.x * 128 + threadIdx.x, b = blockIdx.y;
-    if (d >= a.D) return;
-    const int len = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
-    const T* g = static_cast<const T*>(a.gate) + b * a.gs[0] + d;
-    const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + d;
-    T* y = static_cast<T*>(a.y) + (int64_t)b * a.N * a.D + d;
-    float h = a.first ? a.first[(int64_t)b * a.D + d] : 0.f;
-    for (int t = 0; t < a.N; ++t) {
-        float out = 0.f;
-        if (t < len) {
-            float al, keep;
-            gates(to_float(g[t * a.gs[1]]), al, keep);
-            const float v = to_float(x[t * a.xs[1]]);
-            out = h = fmaf(al, h, a.coupled ? keep * v : v);
-        }
-        y[(int64_t)t * a.D] = round_to<T>(out);
-    }
-    if (a.end) a.end[(int64_t)b * a.D + d] = h;
+#ifndef SCAN_CTAS
+#define SCAN_CTAS 2
+#endif
+// The scan.  A CTA takes 32 channels and a chunk of tokens, a cluster of CTAs
+// neighbouring chunks; it walks the sequence (backwards for the gradient) in
+// strides of a cluster's chunks.  Over tokens in walking order both directions
+// are c <- A c + b: forward A = a, b = s x, c = h; backward A = a, b = a dh,
+// c = a G.  A thread holds V channels of R neighbouring tokens in registers
+// and
+//   1. forms (prod A, the end from c = 0) of its tokens,
+//   2. joins it with its warp's other token groups by shuffles, with the other
+//      warps through shared memory, with the cluster's other CTAs through
+//      theirs (each CTA writes its total into all of them, one cluster barrier),
+//   3. folds what precedes it into the carried state, in an order that depends
+//      on the sizes alone, and walks its tokens again to write the outputs.
+// So each input is read and each output written once, whatever the length.
+// The tokens arrive by asynchronous copies, two chunks deep, each thread's
+// into slots that it alone reads; only pieces under 4 bytes (single bf16
+// channels, where width or alignment is odd) are loaded directly.
+//
+// Cluster barriers wait in hardware for CTAs that were launched together;
+// every thread of every CTA takes the same number of them.
+constexpr int kTile = 32;     // channels of a CTA
+constexpr int kStages = 2;
+constexpr int kMaxCluster = 8;
+
+template <typename T, int V>
+struct alignas(V * sizeof(T)) Chans {
+    T v[V];
+};
+
+template <int BYTES>
+__device__ __forceinline__ void fetch_async(void* dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(BYTES)
+                     : "memory");
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) scan_channel_backward_kernel(const __grid_constant__ ScanArgs a) {
-    const int d = blockIdx.x * 128 + threadIdx.x, b = blockIdx.y;
-    if (d >= a.D) return;
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Stores to the same shared-memory address of another CTA of the cluster.
+__device__ __forceinline__ void store_remote(float2* mine, int rank, float2 v) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(mine)), "r"(rank));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+}
+
+template <typename T, bool BWD>
+constexpr int elements() {  // of a thread and chunk: 32 KB of tokens a stage
+    return 32 / (int)sizeof(T) / (BWD ? 2 : 1) * 2;
+}
+
+template <typename T, int V, bool BWD>
+__global__ void __launch_bounds__(256, SCAN_CTAS)
+scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int rounds) {
+    constexpr int LC = kTile / V, GROUPS = 32 / LC;   // lanes of a token; token groups of a warp
+    constexpr int R = elements<T, BWD>() / V;         // tokens of a thread
+    constexpr int CT = 8 * GROUPS * R;                // tokens of a chunk
+    constexpr int K = BWD ? 4 : 2;                    // gate, x, h before, dh
+    constexpr bool kAsync = V * sizeof(T) >= 4;
+    using Piece = Chans<T, V>;
+    extern __shared__ __align__(16) unsigned char raw[];
+    Piece* slots = reinterpret_cast<Piece*>(raw);     // [stage][array][token][thread]
+    __shared__ float2 warps[2][8][kTile];             // a warp's (A, b), per parity of the round
+    __shared__ float2 ctas[2][kMaxCluster][kTile];    // a CTA's, written by it into every CTA
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x % cluster;
+    const int tile = blockIdx.x / cluster % tiles, b = blockIdx.x / cluster / tiles;
+    const int d0 = tile * kTile, ch = lane % LC * V, d = d0 + ch;
+    const bool on = d < a.D;                          // V divides D where V > 1
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
-    const T* g = static_cast<const T*>(a.gate) + b * a.gs[0] + d;
-    const T* x = static_cast<const T*>(a.x) + b * a.xs[0] + d;
-    const T* h = static_cast<const T*>(a.h) + (int64_t)b * a.N * a.D + d;
-    const T* dh = static_cast<const T*>(a.dh) + (int64_t)b * a.N * a.D + d;
-    T* dg = static_cast<T*>(a.dgate) + b * a.dgs[0] + d;
-    T* dx = static_cast<T*>(a.dx) + b * a.dxs[0] + d;
-    float c = a.last ? a.last[(int64_t)b * a.D + d] : 0.f;
-    const float h0 = a.first ? a.first[(int64_t)b * a.D + d] : 0.f;
-    for (int t = a.N - 1; t >= 0; --t) {
-        float og = 0.f, ox = 0.f;
-        if (t < len) {
-            float al, keep;
-            gates(to_float(g[t * a.gs[1]]), al, keep);
-            const float v = to_float(x[t * a.xs[1]]);
-            const float before = t ? to_float(h[(int64_t)(t - 1) * a.D]) : h0;
-            const float G = to_float(dh[(int64_t)t * a.D]) + c;
-            og = G * (a.coupled ? before - v : before) * (al * keep);
-            ox = a.coupled ? G * keep : G;
-            c = al * G;
-        }
-        dg[t * a.dgs[1]] = round_to<T>(og);
-        dx[t * a.dxs[1]] = round_to<T>(ox);
+    const int first = (warp * GROUPS + lane / LC) * R;  // of this thread's tokens in the chunk, in walking order
+
+    // lane l of every warp carries channel d0 + l of the state
+    const bool chan = d0 + lane < a.D;
+    const int64_t state = (int64_t)b * a.D + d0 + lane;
+    const float* init = BWD ? a.last : a.first;
+    float run = init && chan ? init[state] : 0.f;
+
+    const T* src[K];
+    int64_t step[K];
+    src[0] = static_cast<const T*>(a.gate) + b * a.gs[0] + d, step[0] = a.gs[1];
+    src[1] = static_cast<const T*>(a.x) + b * a.xs[0] + d, step[1] = a.xs[1];
+    const int64_t dense = (int64_t)b * a.N * a.D + d;
+    if constexpr (BWD) {
+        src[2] = static_cast<const T*>(a.h) + dense - a.D, step[2] = a.D;
+        src[3] = static_cast<const T*>(a.dh) + dense, step[3] = a.D;
     }
-    if (a.end) a.end[(int64_t)b * a.D + d] = c;
+    auto token = [&](int round, int r) {  // the token that walks r-th in this thread's run
+        const unsigned s = ((unsigned)round * cluster + rank) * CT + first + r;  // past 2^31 in the last round at most
+        return (int)(BWD ? (unsigned)a.N - 1u - s : s);
+    };
+    auto used = [&](int t, int k) { return on && t >= (k == 2 ? 1 : 0) && t < len; };
+    auto inside = [&](int t) { return on && (unsigned)t < (unsigned)a.N; };
+    auto fetch = [&](int round) {
+        if constexpr (kAsync) {
+            if (round < rounds) {
+                Piece* to = slots + (round % kStages) * K * R * 256 + tid;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const int t = token(round, r);
+                        if (used(t, k)) fetch_async<sizeof(Piece)>(to + (k * R + r) * 256, src[k] + t * step[k]);
+                    }
+            }
+            ptx::cp_async_commit();
+        }
+    };
+    auto piece = [&](int round, int k, int r) {
+        if constexpr (kAsync) {
+            return slots[((round % kStages) * K + k) * R * 256 + r * 256 + tid];
+        } else {
+            Piece p;
+            p.v[0] = src[k][token(round, r) * step[k]];
+            return p;
+        }
+    };
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    if (cluster > 1) cluster_barrier();  // no CTA writes into one that has not started
+
+    for (int round = 0; round < rounds; ++round) {
+        fetch(round + kStages - 1);
+        ptx::cp_async_wait<kStages - 1>();
+        // 1. this thread's tokens: A and b of each, and their join
+        float A[R][V], Bv[R][V], keep[BWD ? R : 1][V];
+        float pa[V], pb[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) pa[v] = 1.f, pb[v] = 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = token(round, r);
+            Piece g = {}, q = {};
+            const bool u = used(t, 0);
+            if (u) g = piece(round, 0, r), q = piece(round, BWD ? 3 : 1, r);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float al, kp;
+                gates<T>(to_float(g.v[v]), al, kp);
+                const float w = to_float(q.v[v]);
+                A[r][v] = u ? al : 1.f;
+                Bv[r][v] = !u ? 0.f : BWD ? w : a.coupled ? kp * w : w;
+                if constexpr (BWD) keep[r][v] = kp;
+                pb[v] = BWD ? A[r][v] * (Bv[r][v] + pb[v]) : fmaf(A[r][v], pb[v], Bv[r][v]);
+                pa[v] *= A[r][v];
+            }
+        }
+        // 2. within the warp: inclusive over its token groups, then exclusive
+#pragma unroll
+        for (int o = LC; o < 32; o <<= 1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float ba = __shfl_up_sync(0xffffffffu, pa[v], o), bb = __shfl_up_sync(0xffffffffu, pb[v], o);
+                if (lane >= o) {
+                    pb[v] = fmaf(pa[v], bb, pb[v]);
+                    pa[v] *= ba;
+                }
+            }
+        }
+        const int par = round & 1;
+        if (lane >= 32 - LC) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) warps[par][warp][ch + v] = make_float2(pa[v], pb[v]);
+        }
+        if constexpr (GROUPS > 1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float ba = __shfl_up_sync(0xffffffffu, pa[v], LC), bb = __shfl_up_sync(0xffffffffu, pb[v], LC);
+                pa[v] = lane >= LC ? ba : 1.f;
+                pb[v] = lane >= LC ? bb : 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) pa[v] = 1.f, pb[v] = 0.f;
+        }
+        __syncthreads();
+        // across warps and CTAs, lane l for channel l: c is the state before this warp's tokens
+        float c = run;
+        if (cluster > 1) {
+            if (warp == 0) {
+                float2 all = warps[par][0][lane];
+#pragma unroll
+                for (int w = 1; w < 8; ++w) {
+                    const float2 p = warps[par][w][lane];
+                    all = make_float2(all.x * p.x, fmaf(p.x, all.y, p.y));
+                }
+                for (int i = 0; i < cluster; ++i) store_remote(&ctas[par][rank][lane], i, all);
+            }
+            cluster_barrier();
+            for (int i = 0; i < cluster; ++i) {
+                if (i == rank) c = run;
+                const float2 p = ctas[par][i][lane];
+                run = fmaf(p.x, run, p.y);
+            }
+#pragma unroll
+            for (int w = 0; w < 7; ++w)
+                if (w < warp) {
+                    const float2 p = warps[par][w][lane];
+                    c = fmaf(p.x, c, p.y);
+                }
+        } else {
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w == warp) c = run;
+                const float2 p = warps[par][w][lane];
+                run = fmaf(p.x, run, p.y);
+            }
+        }
+        // 3. the outputs
+        float s[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = fmaf(pa[v], __shfl_sync(0xffffffffu, c, ch + v), pb[v]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int t = token(round, r);
+            const bool u = used(t, 0);
+            if constexpr (!BWD) {
+                Piece o;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    s[v] = fmaf(A[r][v], s[v], Bv[r][v]);
+                    o.v[v] = round_to<T>(u ? s[v] : 0.f);
+                }
+                if (inside(t)) *reinterpret_cast<Piece*>(static_cast<T*>(a.y) + dense + (int64_t)t * a.D) = o;
+            } else {
+                Piece og, ox, x = {}, hb = {};
+                if (u) x = piece(round, 1, r);
+                if (used(t, 2)) hb = piece(round, 2, r);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    float before = to_float(hb.v[v]);
+                    if (t == 0 && a.first && on) before = a.first[(int64_t)b * a.D + d + v];
+                    const float G = Bv[r][v] + s[v];
+                    s[v] = A[r][v] * G;
+                    const float diff = a.coupled ? before - to_float(x.v[v]) : before;
+                    og.v[v] = round_to<T>(u ? s[v] * keep[r][v] * diff : 0.f);
+                    ox.v[v] = round_to<T>(!u ? 0.f : a.coupled ? G * keep[r][v] : G);
+                }
+                if (inside(t)) {
+                    *reinterpret_cast<Piece*>(static_cast<T*>(a.dgate) + b * a.dgs[0] + t * a.dgs[1] + d) = og;
+                    *reinterpret_cast<Piece*>(static_cast<T*>(a.dx) + b * a.dxs[0] + t * a.dxs[1] + d) = ox;
+                }
+            }
+        }
+    }
+    if (a.end && rank == 0 && warp == 0 && chan) a.end[state] = run;
+}
+
+template <typename T, bool BWD>
+bool in_pieces(const ScanArgs& a, int V) {
+    const size_t bytes = V * sizeof(T);
+    if (a.D % V != 0) return false;
+    const void* p[] = {a.gate, a.x, a.h, a.dh, a.y, a.dgate, a.dx};
+    for (const void* q : p)
+        if (q && !entry::aligned(q, bytes)) return false;
+    for (int i = 0; i < 2; ++i)
+        if (a.gs[i] % V || a.xs[i] % V || (BWD && (a.dgs[i] % V || a.dxs[i] % V))) return false;
+    return true;
+}
+
+template <typename T, int V, bool BWD>
+cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
+    constexpr int CT = 8 * elements<T, BWD>();  // 8 warps x 32 lanes x elements / 32 channels
+    constexpr size_t smem = V * sizeof(T) >= 4 ? (size_t)kStages * (BWD ? 4 : 2) * elements<T, BWD>() * sizeof(T) * 256 : 0;
+    const int64_t tiles = (a.D + kTile - 1) / kTile, work = tiles * a.B;
+    const int64_t chunks = (a.N + CT - 1) / CT;
+    // CTAs that fit at once share a sequence while there are more of them than
+    // channel tiles
+    int64_t cluster = (int64_t)entry::num_sms() * SCAN_CTAS / work;
+    if (cluster > chunks) cluster = chunks;
+    if (cluster > kMaxCluster) cluster = kMaxCluster;
+    if (cluster < 1) cluster = 1;
+    if (work * cluster >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
+    const int rounds = (int)((chunks + cluster - 1) / cluster);
+    auto kernel = scan_kernel<T, V, BWD>;
+    if (smem > 0) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(work * cluster));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e;
+    TA_TIMED(stream, BWD ? "scan_kernel_backward" : "scan_kernel_forward",
+             e = cudaLaunchKernelEx(&cfg, kernel, a, (int)tiles, (int)cluster, rounds));
+    return e;
 }
 
 template <typename T, bool BWD>
 cudaError_t launch_scan(const ScanArgs& a, cudaStream_t stream) {
-    const dim3 grid((a.D + 127) / 128, a.B);
-    if (BWD) {
-        TA_TIMED(stream, "scan_channel_backward_kernel", scan_channel_backward_kernel<T><<<grid, 128, 0, stream>>>(a));
-    } else {
-        TA_TIMED(stream, "scan_channel_kernel", scan_channel_kernel<T><<<grid, 128, 0, stream>>>(a));
-    }
-    return cudaGetLastError();
+    if (in_pieces<T, BWD>(a, 4)) return launch_scan_v<T, 4, BWD>(a, stream);
+    if (in_pieces<T, BWD>(a, 2)) return launch_scan_v<T, 2, BWD>(a, stream);
+    return launch_scan_v<T, 1, BWD>(a, stream);
 }
 
 // One token: VE channels a thread.
@@ -141,7 +395,7 @@ gated_step_kernel(const T* __restrict__ gate, const T* __restrict__ x, const flo
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
             float a, keep;
-            gates(to_float(g[e]), a, keep);
+            gates<T>(to_float(g[e]), a, keep);
             const float xv = to_float(v[e]);
             s[e] = fmaf(a, s[e], coupled ? keep * xv : xv);
             o[e] = round_to<T>(s[e]);

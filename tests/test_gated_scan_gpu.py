@@ -174,7 +174,16 @@ def test_infinite_gates_reset_and_hold(dtype):
     gate[0, 100], gate[0, 200] = float("-inf"), float("inf")
     h, last = SCAN[dtype](gate, x, h0=h0, h_last=True)
     fresh, fresh_last = SCAN[dtype](gate[:, 100:], x[:, 100:], h_last=True)
-    assert torch.equal(h[:, 100], x[:, 100]) and torch.equal(h[:, 200], h[:, 199])
+    assert torch.equal(h[:, 100], x[:, 100])
+    # token 200 may open another run of tokens than 199 closes: the state that enters it is then (prod a) c + b of
+    # the run before, 199's own value the same sum walked token by token; both are within E of the exact state (the
+    # module's analysis, which counts the sums' and the state's roundings), so they are within 2 E of one another,
+    # and a rounding to the type each
+    finite = gate.clone()
+    finite[0, 100], finite[0, 200] = -9, 9
+    E, _ = _bounds(finite, x, True, h0, None)
+    apart = np.abs(f64(h[:, 200]) - f64(h[:, 199]))
+    assert (apart <= 2 * E[:, 199] + 2 * (_half(dtype) if dtype == "bf16" else 0) * np.abs(f64(h[:, 199]))).all()
     torch.testing.assert_close(h[:, 100:], fresh, rtol=2 * _half(dtype) + 1e-4 * (dtype == "f32"), atol=1e-5)
     dgate, dx, _ = BACK[dtype](gate, x, h, dh, h0=h0, dh_last=dl)
     assert torch.isfinite(dgate).all() and torch.isfinite(dx).all()
