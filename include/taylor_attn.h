@@ -378,7 +378,7 @@ TAYLOR_API int64_t taylor_attn_prefill_noalloc_scratch_floats(void);
  * all prior work), stores it in *flags, clears it when clear != 0, and
  * returns TAYLOR_ERR_TIMEOUT if any bit was set, else TAYLOR_OK.
  * Bits: 1 = decode state load, 2 = decode state store, 4 = prefill pipeline,
- * 8 = taylor_attn_selftest_bounded_wait. */
+ * 8 = taylor_attn_selftest_bounded_wait, 16 = gated scan. */
 TAYLOR_API int taylor_attn_device_errors(int clear, unsigned int* flags);
 
 /* Exercises the timeout path on the device: one block waits on an mbarrier

@@ -12,14 +12,19 @@
 // that it keeps its digits where a is near 1.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "entry.h"
 #include "internal.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace ta {
 
 namespace {
+
+constexpr unsigned int kErrScanWait = 16u;  // bit of the device error word
 
 struct ScanArgs {
     const void *gate, *x, *h, *dh;     // h, dh: backward
@@ -54,6 +59,30 @@ __device__ __forceinline__ void gates(float g, float& a, float& keep) {
 }
 
 template <typename T>
+__device__ __forceinline__ void gates(f32x2 g, f32x2& a, f32x2& keep) {
+    if constexpr (sizeof(T) == 2) {
+        float2 t = split2(mul2(g, make2(-1.4426950408889634f, -1.4426950408889634f))), e;
+        asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(t.x));
+        asm("min.NaN.f32 %0, %0, 0f42FC0000;" : "+f"(t.y));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+        const f32x2 e2 = make2(e.x, e.y);
+        t = split2(add2(e2, make2(1.0f, 1.0f)));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+        a = make2(e.x, e.y);
+        keep = mul2(e2, a);
+    } else {
+        const float2 x = split2(g);
+        float2 al, kp;
+        gates<T>(x.x, al.x, kp.x);
+        gates<T>(x.y, al.y, kp.y);
+        a = make2(al.x, al.y);
+        keep = make2(kp.x, kp.y);
+    }
+}
+
+template <typename T>
 __device__ __forceinline__ T round_to(float x);
 template <>
 __device__ __forceinline__ float round_to<float>(float x) { return x; }
@@ -72,7 +101,8 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 //   1. forms (prod A, the end from c = 0) of its tokens,
 //   2. joins it with its warp's other token groups by shuffles, with the other
 //      warps through shared memory, with the cluster's other CTAs through
-//      theirs (each CTA writes its total into all of them, one cluster barrier),
+//      theirs: each CTA sends its total to all of them by stores that count
+//      their bytes on the receiver's barrier, so no fence waits for outputs,
 //   3. folds what precedes it into the carried state, in an order that depends
 //      on the sizes alone, and walks its tokens again to write the outputs.
 // So each input is read and each output written once, whatever the length.
@@ -80,16 +110,98 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 // into slots that it alone reads; only pieces under 4 bytes (single bf16
 // channels, where width or alignment is odd) are loaded directly.
 //
-// Cluster barriers wait in hardware for CTAs that were launched together;
-// every thread of every CTA takes the same number of them.
+// The CTAs of a cluster run at the same time, and each sends before it waits.
+// The totals' buffers alternate: a CTA sends those of round i + 2 only after it
+// has those of round i + 1, which every CTA sends after a CTA barrier behind
+// its reads of round i.
 constexpr int kTile = 32;     // channels of a CTA
 constexpr int kStages = 2;
 constexpr int kMaxCluster = 8;
+constexpr uint32_t kWait = 1u << 24;  // polls of a cluster's totals
 
 template <typename T, int V>
 struct alignas(V * sizeof(T)) Chans {
     T v[V];
 };
+
+// V channels in arithmetic: pairs, or one value.
+template <int V>
+struct Lanes {
+    f32x2 e[V / 2];
+};
+template <>
+struct Lanes<1> {
+    float e[1];
+};
+template <int V>
+constexpr int kPairs = V == 1 ? 1 : V / 2;
+
+__device__ __forceinline__ void spread(float v, float& out) { out = v; }
+__device__ __forceinline__ void spread(float v, f32x2& out) { out = make2(v, v); }
+
+template <int V>
+__device__ __forceinline__ Lanes<V> lanes_of(float v) {
+    Lanes<V> r;
+#pragma unroll
+    for (int i = 0; i < kPairs<V>; ++i) spread(v, r.e[i]);
+    return r;
+}
+template <int V>
+__device__ __forceinline__ void unpack(const Chans<float, V>& p, Lanes<V>& r) {
+    if constexpr (V == 1) {
+        r.e[0] = p.v[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.e[i] = make2(p.v[2 * i], p.v[2 * i + 1]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void unpack(const Chans<__nv_bfloat16, V>& p, Lanes<V>& r) {
+    if constexpr (V == 1) {
+        r.e[0] = __bfloat162float(p.v[0]);
+    } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.e[i] = make2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+}
+template <int V>
+__device__ __forceinline__ void values(const Lanes<V>& r, float (&x)[V]) {
+    if constexpr (V == 1) {
+        x[0] = r.e[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) {
+            const float2 f = split2(r.e[i]);
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        }
+    }
+}
+template <int V>
+__device__ __forceinline__ Lanes<V> lanes_of(const float (&x)[V]) {
+    Lanes<V> r;
+    if constexpr (V == 1) {
+        r.e[0] = x[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) r.e[i] = make2(x[2 * i], x[2 * i + 1]);
+    }
+    return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ Chans<T, V> pack(const Lanes<V>& r) {
+    float x[V];
+    values<V>(r, x);
+    Chans<T, V> p;
+    if constexpr (sizeof(T) == 2 && V > 1) {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) *reinterpret_cast<__nv_bfloat162*>(&p.v[i]) = __floats2bfloat162_rn(x[i], x[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p.v[i] = round_to<T>(x[i]);
+    }
+    return p;
+}
 
 template <int BYTES>
 __device__ __forceinline__ void fetch_async(void* dst, const void* src) {
@@ -100,16 +212,15 @@ __device__ __forceinline__ void fetch_async(void* dst, const void* src) {
                      : "memory");
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Stores to the same shared-memory address of another CTA of the cluster.
-__device__ __forceinline__ void store_remote(float2* mine, int rank, float2 v) {
-    uint32_t at;
+// Stores to the same shared-memory address of CTA `rank` of the cluster and
+// counts the bytes on that CTA's barrier.
+__device__ __forceinline__ void send(float2* mine, uint64_t* bar, int rank, float2 v) {
+    uint32_t at, to;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(mine)), "r"(rank));
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(ptx::smem_u32(bar)), "r"(rank));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(at),
+                 "f"(v.x), "f"(v.y), "r"(to)
+                 : "memory");
 }
 
 template <typename T, bool BWD>
@@ -119,17 +230,19 @@ constexpr int elements() {  // of a thread and chunk: 32 KB of tokens a stage
 
 template <typename T, int V, bool BWD>
 __global__ void __launch_bounds__(256, SCAN_CTAS)
-scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int rounds) {
+scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int rounds, unsigned int* err) {
     constexpr int LC = kTile / V, GROUPS = 32 / LC;   // lanes of a token; token groups of a warp
     constexpr int R = elements<T, BWD>() / V;         // tokens of a thread
     constexpr int CT = 8 * GROUPS * R;                // tokens of a chunk
     constexpr int K = BWD ? 4 : 2;                    // gate, x, h before, dh
+    constexpr int P = kPairs<V>;
     constexpr bool kAsync = V * sizeof(T) >= 4;
     using Piece = Chans<T, V>;
     extern __shared__ __align__(16) unsigned char raw[];
     Piece* slots = reinterpret_cast<Piece*>(raw);     // [stage][array][token][thread]
     __shared__ float2 warps[2][8][kTile];             // a warp's (A, b), per parity of the round
-    __shared__ float2 ctas[2][kMaxCluster][kTile];    // a CTA's, written by it into every CTA
+    __shared__ float2 ctas[2][kMaxCluster][kTile];    // a CTA's, sent by it to every CTA
+    __shared__ __align__(8) uint64_t bars[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % cluster;
     const int tile = blockIdx.x / cluster % tiles, b = blockIdx.x / cluster / tiles;
@@ -138,11 +251,23 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
     const int first = (warp * GROUPS + lane / LC) * R;  // of this thread's tokens in the chunk, in walking order
 
+    if (cluster > 1) {
+        if (tid == 0) {
+            ptx::mbar_init(&bars[0], 1);
+            ptx::mbar_init(&bars[1], 1);
+            ptx::fence_mbar_init();
+        }
+        // no CTA sends to one that has not started
+        __syncthreads();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     // lane l of every warp carries channel d0 + l of the state
     const bool chan = d0 + lane < a.D;
     const int64_t state = (int64_t)b * a.D + d0 + lane;
     const float* init = BWD ? a.last : a.first;
     float run = init && chan ? init[state] : 0.f;
+    bool lost = false;  // a wait ran out
 
     const T* src[K];
     int64_t step[K];
@@ -153,9 +278,16 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         src[2] = static_cast<const T*>(a.h) + dense - a.D, step[2] = a.D;
         src[3] = static_cast<const T*>(a.dh) + dense, step[3] = a.D;
     }
-    auto token = [&](int round, int r) {  // the token that walks r-th in this thread's run
-        const unsigned s = ((unsigned)round * cluster + rank) * CT + first + r;  // past 2^31 in the last round at most
+    constexpr int DIR = BWD ? -1 : 1;
+    // the token that walks first in this thread's run
+    auto token = [&](int round) {
+        const unsigned s = ((unsigned)round * cluster + rank) * CT + first;  // past 2^31 in the last round at most
         return (int)(BWD ? (unsigned)a.N - 1u - s : s);
+    };
+    // whether every token and channel of this CTA's chunk exists, and (backward) has one before it
+    auto whole = [&](int round) {
+        const int64_t s = ((int64_t)round * cluster + rank) * CT;
+        return d0 + kTile <= a.D && (BWD ? a.N - s <= len && a.N - s - CT >= 1 : s + CT <= len);
     };
     auto used = [&](int t, int k) { return on && t >= (k == 2 ? 1 : 0) && t < len; };
     auto inside = [&](int t) { return on && (unsigned)t < (unsigned)a.N; };
@@ -163,108 +295,118 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         if constexpr (kAsync) {
             if (round < rounds) {
                 Piece* to = slots + (round % kStages) * K * R * 256 + tid;
+                const int t0 = token(round);
+                const bool all = whole(round);
 #pragma unroll
-                for (int k = 0; k < K; ++k)
+                for (int k = 0; k < K; ++k) {
+                    const T* p = src[k] + t0 * step[k];
+                    if (all) {
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const int t = token(round, r);
-                        if (used(t, k)) fetch_async<sizeof(Piece)>(to + (k * R + r) * 256, src[k] + t * step[k]);
+                        for (int r = 0; r < R; ++r, p += DIR * step[k]) fetch_async<sizeof(Piece)>(to + (k * R + r) * 256, p);
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < R; ++r, p += DIR * step[k])
+                            if (used(t0 + DIR * r, k)) fetch_async<sizeof(Piece)>(to + (k * R + r) * 256, p);
                     }
+                }
             }
             ptx::cp_async_commit();
         }
     };
-    auto piece = [&](int round, int k, int r) {
-        if constexpr (kAsync) {
-            return slots[((round % kStages) * K + k) * R * 256 + r * 256 + tid];
-        } else {
-            Piece p;
-            p.v[0] = src[k][token(round, r) * step[k]];
-            return p;
-        }
-    };
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
-    if (cluster > 1) cluster_barrier();  // no CTA writes into one that has not started
 
     for (int round = 0; round < rounds; ++round) {
+        const int par = round & 1;
+        if (cluster > 1 && tid == 0) ptx::mbar_arrive_expect_tx(&bars[par], cluster * kTile * 8);
         fetch(round + kStages - 1);
         ptx::cp_async_wait<kStages - 1>();
+        const int t0 = token(round);
+        const Piece* mine = slots + (round % kStages) * K * R * 256 + tid;
+        auto piece = [&](int k, int r) {
+            if constexpr (kAsync) return mine[(k * R + r) * 256];
+            else return *reinterpret_cast<const Piece*>(src[k] + (t0 + DIR * r) * step[k]);
+        };
+        const bool all = whole(round);
         // 1. this thread's tokens: A and b of each, and their join
-        float A[R][V], Bv[R][V], keep[BWD ? R : 1][V];
-        float pa[V], pb[V];
+        Lanes<V> A[R], Bv[R], keep[BWD ? R : 1];
+        Lanes<V> pa = lanes_of<V>(1.f), pb = lanes_of<V>(0.f);
+        auto gather = [&](auto every) {
+            Piece g[R], q[R];
 #pragma unroll
-        for (int v = 0; v < V; ++v) pa[v] = 1.f, pb[v] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int t = token(round, r);
-            Piece g = {}, q = {};
-            const bool u = used(t, 0);
-            if (u) g = piece(round, 0, r), q = piece(round, BWD ? 3 : 1, r);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float al, kp;
-                gates<T>(to_float(g.v[v]), al, kp);
-                const float w = to_float(q.v[v]);
-                A[r][v] = u ? al : 1.f;
-                Bv[r][v] = !u ? 0.f : BWD ? w : a.coupled ? kp * w : w;
-                if constexpr (BWD) keep[r][v] = kp;
-                pb[v] = BWD ? A[r][v] * (Bv[r][v] + pb[v]) : fmaf(A[r][v], pb[v], Bv[r][v]);
-                pa[v] *= A[r][v];
+            for (int r = 0; r < R; ++r) {
+                g[r] = q[r] = Piece{};
+                if (every || used(t0 + DIR * r, 0)) g[r] = piece(0, r), q[r] = piece(BWD ? 3 : 1, r);
             }
-        }
-        // 2. within the warp: inclusive over its token groups, then exclusive
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const bool u = every || used(t0 + DIR * r, 0);
+                Lanes<V> gv, qv;
+                unpack(g[r], gv);
+                unpack(q[r], qv);
+                if (!u) A[r] = lanes_of<V>(1.f), Bv[r] = lanes_of<V>(0.f);
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    auto& kp = keep[BWD ? r : 0].e[i];
+                    if (u) {
+                        gates<T>(gv.e[i], A[r].e[i], kp);
+                        Bv[r].e[i] = !BWD && a.coupled ? mul2(kp, qv.e[i]) : qv.e[i];
+                    } else if (BWD) {
+                        spread(0.f, kp);
+                    }
+                    pb.e[i] = BWD ? mul2(A[r].e[i], add2(Bv[r].e[i], pb.e[i])) : fma2(A[r].e[i], pb.e[i], Bv[r].e[i]);
+                    pa.e[i] = mul2(pa.e[i], A[r].e[i]);
+                }
+            }
+        };
+        if (all) gather(std::true_type{});
+        else gather(std::false_type{});
+        // 2. within the warp, over its token groups
+        float ea[V], eb[V];
+        values<V>(pa, ea);
+        values<V>(pb, eb);
 #pragma unroll
         for (int o = LC; o < 32; o <<= 1) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const float ba = __shfl_up_sync(0xffffffffu, pa[v], o), bb = __shfl_up_sync(0xffffffffu, pb[v], o);
+                const float ba = __shfl_up_sync(0xffffffffu, ea[v], o), bb = __shfl_up_sync(0xffffffffu, eb[v], o);
                 if (lane >= o) {
-                    pb[v] = fmaf(pa[v], bb, pb[v]);
-                    pa[v] *= ba;
+                    eb[v] = fmaf(ea[v], bb, eb[v]);
+                    ea[v] *= ba;
                 }
             }
         }
-        const int par = round & 1;
         if (lane >= 32 - LC) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) warps[par][warp][ch + v] = make_float2(pa[v], pb[v]);
-        }
-        if constexpr (GROUPS > 1) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float ba = __shfl_up_sync(0xffffffffu, pa[v], LC), bb = __shfl_up_sync(0xffffffffu, pb[v], LC);
-                pa[v] = lane >= LC ? ba : 1.f;
-                pb[v] = lane >= LC ? bb : 0.f;
-            }
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) pa[v] = 1.f, pb[v] = 0.f;
+            for (int v = 0; v < V; ++v) warps[par][warp][ch + v] = make_float2(ea[v], eb[v]);
         }
         __syncthreads();
         // across warps and CTAs, lane l for channel l: c is the state before this warp's tokens
         float c = run;
         if (cluster > 1) {
             if (warp == 0) {
-                float2 all = warps[par][0][lane];
+                float2 total = warps[par][0][lane];
 #pragma unroll
                 for (int w = 1; w < 8; ++w) {
                     const float2 p = warps[par][w][lane];
-                    all = make_float2(all.x * p.x, fmaf(p.x, all.y, p.y));
+                    total = make_float2(total.x * p.x, fmaf(p.x, total.y, p.y));
                 }
-                for (int i = 0; i < cluster; ++i) store_remote(&ctas[par][rank][lane], i, all);
+                for (int i = 0; i < cluster; ++i) send(&ctas[par][rank][lane], &bars[par], i, total);
             }
-            cluster_barrier();
+            float2 before[7];
+#pragma unroll
+            for (int w = 0; w < 7; ++w) before[w] = w < warp ? warps[par][w][lane] : make_float2(1.f, 0.f);
+            if (!lost && !ptx::mbar_wait(&bars[par], (round >> 1) & 1, kWait)) {
+                // never in a sound run: the outputs from here on are not to be used
+                lost = true;
+                if (lane == 0) atomicOr(err, kErrScanWait);
+            }
             for (int i = 0; i < cluster; ++i) {
                 if (i == rank) c = run;
                 const float2 p = ctas[par][i][lane];
                 run = fmaf(p.x, run, p.y);
             }
 #pragma unroll
-            for (int w = 0; w < 7; ++w)
-                if (w < warp) {
-                    const float2 p = warps[par][w][lane];
-                    c = fmaf(p.x, c, p.y);
-                }
+            for (int w = 0; w < 7; ++w) c = fmaf(before[w].x, c, before[w].y);
         } else {
 #pragma unroll
             for (int w = 0; w < 8; ++w) {
@@ -273,42 +415,69 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
                 run = fmaf(p.x, run, p.y);
             }
         }
-        // 3. the outputs
-        float s[V];
+        // the state before this thread's tokens: where its predecessor group ends
+        float sv[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = fmaf(pa[v], __shfl_sync(0xffffffffu, c, ch + v), pb[v]);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int t = token(round, r);
-            const bool u = used(t, 0);
-            if constexpr (!BWD) {
-                Piece o;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    s[v] = fmaf(A[r][v], s[v], Bv[r][v]);
-                    o.v[v] = round_to<T>(u ? s[v] : 0.f);
-                }
-                if (inside(t)) *reinterpret_cast<Piece*>(static_cast<T*>(a.y) + dense + (int64_t)t * a.D) = o;
-            } else {
-                Piece og, ox, x = {}, hb = {};
-                if (u) x = piece(round, 1, r);
-                if (used(t, 2)) hb = piece(round, 2, r);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float before = to_float(hb.v[v]);
-                    if (t == 0 && a.first && on) before = a.first[(int64_t)b * a.D + d + v];
-                    const float G = Bv[r][v] + s[v];
-                    s[v] = A[r][v] * G;
-                    const float diff = a.coupled ? before - to_float(x.v[v]) : before;
-                    og.v[v] = round_to<T>(u ? s[v] * keep[r][v] * diff : 0.f);
-                    ox.v[v] = round_to<T>(!u ? 0.f : a.coupled ? G * keep[r][v] : G);
-                }
-                if (inside(t)) {
-                    *reinterpret_cast<Piece*>(static_cast<T*>(a.dgate) + b * a.dgs[0] + t * a.dgs[1] + d) = og;
-                    *reinterpret_cast<Piece*>(static_cast<T*>(a.dx) + b * a.dxs[0] + t * a.dxs[1] + d) = ox;
-                }
+        for (int v = 0; v < V; ++v) {
+            const float in = __shfl_sync(0xffffffffu, c, ch + v);
+            sv[v] = in;
+            if constexpr (GROUPS > 1) {
+                const float end = __shfl_up_sync(0xffffffffu, fmaf(ea[v], in, eb[v]), LC);
+                if (lane >= LC) sv[v] = end;
             }
         }
+        // 3. the outputs
+        Lanes<V> s = lanes_of<V>(sv);
+        auto write = [&](auto every) {
+            [[maybe_unused]] T *y = nullptr, *dg = nullptr, *dx = nullptr;
+            if constexpr (BWD) {
+                dg = static_cast<T*>(a.dgate) + b * a.dgs[0] + d + t0 * a.dgs[1];
+                dx = static_cast<T*>(a.dx) + b * a.dxs[0] + d + t0 * a.dxs[1];
+            } else {
+                y = static_cast<T*>(a.y) + dense + (int64_t)t0 * a.D;
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int t = t0 + DIR * r;
+                const bool u = every || used(t, 0);
+                if constexpr (!BWD) {
+#pragma unroll
+                    for (int i = 0; i < P; ++i) s.e[i] = fma2(A[r].e[i], s.e[i], Bv[r].e[i]);
+                    if (every || inside(t)) *reinterpret_cast<Piece*>(y) = u ? pack<T, V>(s) : Piece{};
+                    y += a.D;
+                } else {
+                    Piece px{}, ph{};
+                    if (u) px = piece(1, r);
+                    if (every || used(t, 2)) ph = piece(2, r);
+                    Lanes<V> x, before, og, ox;
+                    unpack(px, x);
+                    unpack(ph, before);
+                    if (!every && t == 0 && a.first && on) {
+                        float f[V];
+#pragma unroll
+                        for (int v = 0; v < V; ++v) f[v] = a.first[(int64_t)b * a.D + d + v];
+                        before = lanes_of<V>(f);
+                    }
+                    const Lanes<V> minus = lanes_of<V>(a.coupled ? -1.f : 0.f);
+#pragma unroll
+                    for (int i = 0; i < P; ++i) {
+                        const auto G = add2(Bv[r].e[i], s.e[i]);
+                        s.e[i] = mul2(A[r].e[i], G);
+                        const auto diff = a.coupled ? fma2(x.e[i], minus.e[i], before.e[i]) : before.e[i];
+                        og.e[i] = mul2(mul2(s.e[i], keep[r].e[i]), diff);
+                        ox.e[i] = a.coupled ? mul2(G, keep[r].e[i]) : G;
+                    }
+                    if (every || inside(t)) {
+                        *reinterpret_cast<Piece*>(dg) = u ? pack<T, V>(og) : Piece{};
+                        *reinterpret_cast<Piece*>(dx) = u ? pack<T, V>(ox) : Piece{};
+                    }
+                    dg -= a.dgs[1];
+                    dx -= a.dxs[1];
+                }
+            }
+        };
+        if (all) write(std::true_type{});
+        else write(std::false_type{});
     }
     if (a.end && rank == 0 && warp == 0 && chan) a.end[state] = run;
 }
@@ -339,6 +508,8 @@ cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
     if (cluster < 1) cluster = 1;
     if (work * cluster >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
     const int rounds = (int)((chunks + cluster - 1) / cluster);
+    unsigned int* err = device_error_word();
+    if (!err) return cudaErrorUnknown;
     auto kernel = scan_kernel<T, V, BWD>;
     if (smem > 0) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -357,7 +528,7 @@ cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
     cfg.numAttrs = 1;
     cudaError_t e;
     TA_TIMED(stream, BWD ? "scan_kernel_backward" : "scan_kernel_forward",
-             e = cudaLaunchKernelEx(&cfg, kernel, a, (int)tiles, (int)cluster, rounds));
+             e = cudaLaunchKernelEx(&cfg, kernel, a, (int)tiles, (int)cluster, rounds, err));
     return e;
 }
 

@@ -24,6 +24,7 @@
 #include "common.cuh"
 #include "entry.h"
 #include "internal.h"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace ta {
@@ -210,29 +211,6 @@ __device__ __forceinline__ void store_piece(void* p, const Piece<W>& r) {
     if constexpr (W == 4) *static_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
     else if constexpr (W == 2) *static_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
     else *static_cast<unsigned int*>(p) = r.w[0];
-}
-// Two fp32 in a register pair: sm_100 multiplies and adds both in one
-// instruction, which this issue-bound kernel lives on.
-typedef unsigned long long f32x2;
-__device__ __forceinline__ f32x2 make2(float lo, float hi) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 split2(f32x2 v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 __device__ __forceinline__ float total2(f32x2 v) {
     const float2 f = split2(v);
