@@ -89,9 +89,6 @@ __device__ __forceinline__ float round_to<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-#ifndef SCAN_CTAS
-#define SCAN_CTAS 2
-#endif
 // The scan.  A CTA takes 32 channels and a chunk of tokens, a cluster of CTAs
 // neighbouring chunks; it walks the sequence (backwards for the gradient) in
 // strides of a cluster's chunks.  Over tokens in walking order both directions
@@ -109,6 +106,13 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 // The tokens arrive by asynchronous copies, two chunks deep, each thread's
 // into slots that it alone reads; only pieces under 4 bytes (single bf16
 // channels, where width or alignment is odd) are loaded directly.
+//
+// Memory bounds the operator, 6 B a value forward and 12 B backward in bf16;
+// this kernel is bound by instructions and the latency of its rounds: 25 and
+// 49 instructions a value, issue slots 54 % taken at 14 warps an SM.  B4 N8192
+// D1024 bf16: 55 us forward (3.7 TB/s), 99 us backward (4.1 TB/s); with checks
+// on every token, scalar arithmetic and a cluster barrier a round 73 and
+// 126 us; one thread a channel 9.8 ms for both.
 //
 // The CTAs of a cluster run at the same time, and each sends before it waits.
 // The totals' buffers alternate: a CTA sends those of round i + 2 only after it
@@ -223,16 +227,25 @@ __device__ __forceinline__ void send(float2* mine, uint64_t* bar, int rank, floa
                  : "memory");
 }
 
-template <typename T, bool BWD>
-constexpr int elements() {  // of a thread and chunk: 32 KB of tokens a stage
-    return 32 / (int)sizeof(T) / (BWD ? 2 : 1) * 2;
+// Elements (tokens x channels) of a thread and chunk: 32 KB of tokens a stage,
+// which two CTAs of 128 registers a thread hold on an SM.  Half as many, at
+// three CTAs, cost a fifth more time: what a round costs whatever its length
+// (the joins, the wait for the cluster) counts twice as often.  Single bf16
+// channels, whose loads nothing runs ahead of, gain from the third CTA.
+template <typename T, int V, bool BWD>
+constexpr bool kSingles = V * sizeof(T) < 4;
+template <typename T, int V, bool BWD>
+constexpr int elements() {
+    return 32 / (int)sizeof(T) / (BWD ? 2 : 1) * (kSingles<T, V, BWD> ? 1 : 2);
 }
+template <typename T, int V, bool BWD>
+constexpr int kCtas = kSingles<T, V, BWD> ? 3 : 2;  // CTAs an SM holds
 
 template <typename T, int V, bool BWD>
-__global__ void __launch_bounds__(256, SCAN_CTAS)
+__global__ void __launch_bounds__(256, kCtas<T, V, BWD>)
 scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int rounds, unsigned int* err) {
     constexpr int LC = kTile / V, GROUPS = 32 / LC;   // lanes of a token; token groups of a warp
-    constexpr int R = elements<T, BWD>() / V;         // tokens of a thread
+    constexpr int R = elements<T, V, BWD>() / V;         // tokens of a thread
     constexpr int CT = 8 * GROUPS * R;                // tokens of a chunk
     constexpr int K = BWD ? 4 : 2;                    // gate, x, h before, dh
     constexpr int P = kPairs<V>;
@@ -360,7 +373,8 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         };
         if (all) gather(std::true_type{});
         else gather(std::false_type{});
-        // 2. within the warp, over its token groups
+        // 2. within the warp, over its token groups (by shuffles: through shared memory it
+        // took 61 us instead of 55, B4 N8192 D1024 bf16)
         float ea[V], eb[V];
         values<V>(pa, ea);
         values<V>(pb, eb);
@@ -496,13 +510,13 @@ bool in_pieces(const ScanArgs& a, int V) {
 
 template <typename T, int V, bool BWD>
 cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
-    constexpr int CT = 8 * elements<T, BWD>();  // 8 warps x 32 lanes x elements / 32 channels
-    constexpr size_t smem = V * sizeof(T) >= 4 ? (size_t)kStages * (BWD ? 4 : 2) * elements<T, BWD>() * sizeof(T) * 256 : 0;
+    constexpr int CT = 8 * elements<T, V, BWD>();  // 8 warps x 32 lanes x elements / 32 channels
+    constexpr size_t smem = V * sizeof(T) >= 4 ? (size_t)kStages * (BWD ? 4 : 2) * elements<T, V, BWD>() * sizeof(T) * 256 : 0;
     const int64_t tiles = (a.D + kTile - 1) / kTile, work = tiles * a.B;
     const int64_t chunks = (a.N + CT - 1) / CT;
     // CTAs that fit at once share a sequence while there are more of them than
     // channel tiles
-    int64_t cluster = (int64_t)entry::num_sms() * SCAN_CTAS / work;
+    int64_t cluster = (int64_t)entry::num_sms() * kCtas<T, V, BWD> / work;
     if (cluster > chunks) cluster = chunks;
     if (cluster > kMaxCluster) cluster = kMaxCluster;
     if (cluster < 1) cluster = 1;
