@@ -344,6 +344,35 @@ TAYLOR_API int taylor_attn_gated_step_f32(const float* gate, const float* x, con
                                           float* state_out, float* out, int B, int D, int64_t gate_stride,
                                           int64_t x_stride, int coupled, cudaStream_t stream);
 
+/* One new token for every sequence of a batch that shares a long prefix
+ * (states are additive across chunks, so the prefix's state serves all of
+ * them).  prefix_state fp32 [H][stride] is the prefix's Taylor state, stride
+ * and layout as taylor_attn_decode (a prefill of the prefix with B = 1 returns
+ * it); it is only read.  A sequence's tokens past the prefix lie in k_cache
+ * [B][H][cap][d_k] and v_cache [B][H][cap][d_v], lengths[b] of them (int32 [B]
+ * on the device).  q, k [B][H][d_k] and v [B][H][d_v] are the new token's; k
+ * and v are appended to the caches at row lengths[b] (lengths itself is left
+ * to the caller), rows behind it are neither read nor written.  out [B][H][d_v]
+ * fp32 is what taylor_attn_decode returns from a state of the prefix and the
+ * sequence's own tokens together: y = (c (.) phi(q))^T S + sum_j K(tau q.k_j)
+ * [v_j | 1] over the cached tokens and the new one, out = y[0:d_v] / y[d_v].
+ * Tensors bf16 (the _f32 variant: fp32), dense, 16-byte aligned; B*H < 2^24,
+ * cap >= 1.  A sequence whose length is outside 0..cap-1 gets NaN outputs,
+ * leaves its caches alone and sets bit 32 of the device error word.  It pays
+ * while a sequence's own tokens take fewer bytes than its state read and
+ * written would: about 500 tokens a head at d_k 16, d_v 64, n 3 in bf16, 4,300
+ * at d_k 64.  Workspace for the shared part as taylor_attn_prefill takes it. */
+TAYLOR_API int taylor_attn_shared_prefix_decode(const void* q, const void* k, const void* v,
+                                                const float* prefix_state, void* k_cache, void* v_cache,
+                                                const int32_t* lengths, float* out, int B, int H, int cap, int d_k,
+                                                int d_v, int n, float tau, cudaStream_t stream);
+
+/* taylor_attn_shared_prefix_decode with fp32 q, k, v and caches. */
+TAYLOR_API int taylor_attn_shared_prefix_decode_f32(const float* q, const float* k, const float* v,
+                                                    const float* prefix_state, float* k_cache, float* v_cache,
+                                                    const int32_t* lengths, float* out, int B, int H, int cap,
+                                                    int d_k, int d_v, int n, float tau, cudaStream_t stream);
+
 /* taylor_attn_prefill_f32 for callers that cannot allocate device memory
  * (a plugin whose host framework owns all device memory, a serving loop that
  * reserves memory up front and must not see an allocation fail mid-step).
@@ -378,7 +407,8 @@ TAYLOR_API int64_t taylor_attn_prefill_noalloc_scratch_floats(void);
  * all prior work), stores it in *flags, clears it when clear != 0, and
  * returns TAYLOR_ERR_TIMEOUT if any bit was set, else TAYLOR_OK.
  * Bits: 1 = decode state load, 2 = decode state store, 4 = prefill pipeline,
- * 8 = taylor_attn_selftest_bounded_wait, 16 = gated scan. */
+ * 8 = taylor_attn_selftest_bounded_wait, 16 = gated scan,
+ * 32 = a shared-prefix decode's length out of range. */
 TAYLOR_API int taylor_attn_device_errors(int clear, unsigned int* flags);
 
 /* Exercises the timeout path on the device: one block waits on an mbarrier

@@ -64,6 +64,8 @@ SIGNATURES = {
     "taylor_attn_gated_scan_backward_f32": (_I, [*[_P] * 10, *[_I] * 3, *[_P] * 4, _I, _P]),
     "taylor_attn_gated_step": (_I, [*[_P] * 5, _I, _I, _I64, _I64, _I, _P]),
     "taylor_attn_gated_step_f32": (_I, [*[_P] * 5, _I, _I, _I64, _I64, _I, _P]),
+    "taylor_attn_shared_prefix_decode": (_I, [*[_P] * 8, *[_I] * 6, _F, _P]),
+    "taylor_attn_shared_prefix_decode_f32": (_I, [*[_P] * 8, *[_I] * 6, _F, _P]),
     "taylor_attn_prefill_f32_noalloc": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "taylor_attn_prefill_noalloc_scratch_floats": (_I64, []),
     "taylor_attn_device_errors": (_I, [_I, _P]),
@@ -619,6 +621,51 @@ def taylor_attn_gated_step(gate, x, state, coupled: bool = True, out=None, state
 def taylor_attn_gated_step_f32(gate, x, state, coupled: bool = True, out=None, state_out=None, stream=None):
     """taylor_attn_gated_step with fp32 tensors."""
     return _gated_step("taylor_attn_gated_step_f32", torch.float32, gate, x, state, coupled, out, state_out, stream)
+
+
+def _shared_prefix_decode(name, dtype, q, k, v, prefix_state, k_cache, v_cache, lengths, n, tau, out, stream):
+    with _on(q, stream):
+        if q.dim() != 3 or k_cache.dim() != 4:
+            raise ValueError("q, k must be [B, H, d_k], v [B, H, d_v] and the caches [B, H, cap, d]")
+        B, H, d_k = q.shape
+        d_v, cap = v.shape[-1], k_cache.shape[2]
+        stride = taylor_attn_state_stride(d_k, d_v, n)
+        if stride < 0:
+            raise TaylorAttnError(TAYLOR_ERR_UNSUPPORTED, name)
+        _need(q, "q", dtype, q.device)
+        _need(k, "k", dtype, q.device, (B, H, d_k))
+        _need(v, "v", dtype, q.device, (B, H, d_v))
+        lead = (1, H) if prefix_state.dim() == 3 else (H,)
+        _need(prefix_state, "prefix_state", torch.float32, q.device, lead + (stride,))
+        _need(k_cache, "k_cache", dtype, q.device, (B, H, cap, d_k))
+        _need(v_cache, "v_cache", dtype, q.device, (B, H, cap, d_v))
+        _need(lengths, "lengths", torch.int32, q.device, (B,))
+        if out is None:
+            out = torch.empty((B, H, d_v), dtype=torch.float32, device=q.device)
+        else:
+            _need(out, "out", torch.float32, q.device, (B, H, d_v))
+        rc = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(v), _ptr(prefix_state), _ptr(k_cache), _ptr(v_cache),
+                                  _ptr(lengths), _ptr(out), B, H, cap, d_k, d_v, n, float(tau), _stream(None))
+    _check(rc, name)
+    return out
+
+
+def taylor_attn_shared_prefix_decode(q, k, v, prefix_state, k_cache, v_cache, lengths, n: int, tau: float, out=None,
+                                     stream=None):
+    """One token per sequence of a batch that shares a prefix: bf16 q, k
+    [B,H,d_k], v [B,H,d_v]; ``prefix_state`` fp32 [H,stride] (or [1,H,stride],
+    as a prefill returns it); the sequences' own tokens in ``k_cache``
+    [B,H,cap,d_k], ``v_cache`` [B,H,cap,d_v], ``lengths`` int32 [B] of them.
+    k and v are appended at row lengths[b]; returns out fp32 [B,H,d_v]."""
+    return _shared_prefix_decode("taylor_attn_shared_prefix_decode", torch.bfloat16, q, k, v, prefix_state, k_cache,
+                                 v_cache, lengths, n, tau, out, stream)
+
+
+def taylor_attn_shared_prefix_decode_f32(q, k, v, prefix_state, k_cache, v_cache, lengths, n: int, tau: float,
+                                         out=None, stream=None):
+    """taylor_attn_shared_prefix_decode with fp32 q, k, v and caches."""
+    return _shared_prefix_decode("taylor_attn_shared_prefix_decode_f32", torch.float32, q, k, v, prefix_state,
+                                 k_cache, v_cache, lengths, n, tau, out, stream)
 
 
 def taylor_attn_release_workspace() -> None:

@@ -122,3 +122,18 @@ def test_gated_step_refuses(over, status):
     a.update(over)
     assert TA.lib().taylor_attn_gated_step(a["gate"], a["x"], a["state"], a["state"], a["out"], a["B"], a["D"],
                                            a["gs"], a["xs"], 1, None) == status
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(B=-1), INV), (dict(H=-1), INV), (dict(cap=-1), INV), (dict(cap=0), INV), (dict(tau=float("inf")), INV),
+    (dict(n=0), UNS), (dict(n=6), UNS), (dict(d=65), UNS), (dict(d=0), UNS), (dict(dv=62), UNS), (dict(dv=260), UNS),
+    (dict(B=1 << 12, H=1 << 12), UNS), (dict(q=None), INV), (dict(state=None), INV), (dict(kc=None), INV),
+    (dict(lengths=None), INV), (dict(out=None), INV), (dict(vc=P + 8), MIS), (dict(state=P + 4), MIS),
+    (dict(lengths=P + 2), MIS), (dict(B=0, q=None), OK), (dict(H=0, out=None), OK),
+])
+def test_shared_prefix_decode_refuses(over, status):
+    a = dict(q=P, k=P, v=P, state=P, kc=P, vc=P, lengths=P, out=P, B=2, H=2, cap=4, d=16, dv=64, n=3, tau=2.0)
+    a.update(over)
+    assert TA.lib().taylor_attn_shared_prefix_decode(
+        a["q"], a["k"], a["v"], a["state"], a["kc"], a["vc"], a["lengths"], a["out"], a["B"], a["H"], a["cap"],
+        a["d"], a["dv"], a["n"], a["tau"], None) == status
