@@ -357,7 +357,7 @@ TAYLOR_API int taylor_attn_gated_step_f32(const float* gate, const float* x, con
  * sequence's own tokens together: y = (c (.) phi(q))^T S + sum_j K(tau q.k_j)
  * [v_j | 1] over the cached tokens and the new one, out = y[0:d_v] / y[d_v].
  * Tensors bf16 (the _f32 variant: fp32), dense, 16-byte aligned; B*H < 2^24,
- * cap >= 1.  A sequence whose length is outside 0..cap-1 gets NaN outputs,
+ * 1 <= cap <= 2^30.  A sequence whose length is outside 0..cap-1 gets NaN outputs,
  * leaves its caches alone and sets bit 32 of the device error word.  It pays
  * while a sequence's own tokens take fewer bytes than its state read and
  * written would: about 500 tokens a head at d_k 16, d_v 64, n 3 in bf16, 4,300

@@ -16,12 +16,15 @@
 #include "entry.h"
 #include "feature_table.cuh"
 #include "internal.h"
+#include "pairs.cuh"
+#include "ptx.cuh"
 
 namespace ta {
 
 namespace {
 
 constexpr unsigned int kErrLength = 32u;  // bit of the device error word
+constexpr int kMaxSplits = 32;            // shares of the features
 
 struct PrefixArgs {
     const void *q, *k, *v;
@@ -29,74 +32,404 @@ struct PrefixArgs {
     void *kc, *vc;            // [B][H][cap][d], [B][H][cap][dv]
     const int32_t* lengths;   // [B]
     float* out;               // [B][H][dv]
+    float* part;              // workspace: the shared part's shares [splits][H][B][dv + 4]
     unsigned int* err;
     int64_t F, stride;
     int B, H, cap, d, dv, n;
     float tau;
 };
 
-// One CTA per sequence and head.
-template <typename T>
-__global__ void __launch_bounds__(256) prefix_head_kernel(const __grid_constant__ PrefixArgs a) {
-    __shared__ float qs[kMaxDk], phi[256], coef[kMaxN], num[kMaxDv + 1];
-    const int tid = threadIdx.x, bh = blockIdx.x, b = bh / a.H, h = bh - b * a.H;
-    const T* q = static_cast<const T*>(a.q) + (int64_t)bh * a.d;
+// ------------------------------------------------------------ the shared part
+// Y = (c (.) Phi(Q)) S for one head: a product of [queries x F] by [F x d_v],
+// its left side formed feature by feature from q.  A CTA takes MB queries, 64
+// columns and a share of the features, 32 at a time; the shares' sums go to
+// the workspace and are joined by the kernel below.  The column d_v of ones
+// (the normaliser) is summed by the threads that form the features.  fp32 FMA
+// throughout: outputs are fp32, and the product is a small part of the call
+// (2 B F (d_v + 1) flops a head against the cache's bytes).
+constexpr int kFeats = 32;    // features a step
+constexpr int kCols = 64;     // columns a CTA
+
+template <typename T, int MB>
+__global__ void __launch_bounds__(256)
+prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles, int btiles, int steps) {
+    constexpr int TM = MB / 16, PER = kFeats * MB / 256;  // queries of a thread; features it forms a step
+    __shared__ __align__(16) float xs[kMaxDk + 1][MB];    // q by entry, row d is 1 (a missing factor)
+    __shared__ __align__(16) float st[2][kFeats][kCols];
+    __shared__ float zt[2][kFeats];
+    __shared__ __align__(16) float phi[kFeats][MB];
+    __shared__ uint32_t code[2][kFeats];
+    __shared__ float weight[2][kFeats];
+    __shared__ float coef[kMaxN];
+    ptx::pdl_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int at = blockIdx.x;
+    const int split = at % splits;
+    at /= splits;
+    const int ct = at % ctiles;
+    at /= ctiles;
+    const int b0 = at % btiles * MB, h = at / btiles;
+    const int c0 = ct * kCols, ncol = min(kCols, a.dv - c0), nq = min(MB, a.B - b0);
+    const int64_t f0 = (int64_t)split * steps * kFeats;
+    const int64_t f1 = min64(a.F, f0 + (int64_t)steps * kFeats);
+    const float* S = a.state + (int64_t)h * a.stride;
+    const PackedFeat* tab = feat_table(a.d, a.n);
+
+    if (tid < a.n) coef[tid] = query_coeff(tid, a.tau);
+    for (int i = tid; i < MB * a.d; i += 256) {
+        const int m = i / a.d, e = i - m * a.d;
+        xs[e][m] = m < nq ? to_float(static_cast<const T*>(a.q)[((int64_t)(b0 + m) * a.H + h) * a.d + e]) : 0.f;
+    }
+    for (int m = tid; m < MB; m += 256) xs[a.d][m] = 1.f;
+    __syncthreads();
+    auto load = [&](int64_t f, int buf) {  // features f .. f + 31 of the state; past f1: zeros
+        for (int i = tid; i < kFeats * (kCols / 4); i += 256) {
+            const int r = i / (kCols / 4), c = i % (kCols / 4) * 4;
+            const bool in = f + r < f1 && c < ncol;
+            ptx::cp_async16(&st[buf][r][c], in ? S + (f + r) * a.dv + c0 + c : S, in ? 16 : 0);
+        }
+        ptx::cp_async_commit();
+    };
+    // a step's descriptors, four a warp: read ahead into registers, put in place later
+    PackedFeat pf = {};
+    float pz = 0.f;
+    const int dr = warp * (kFeats / 8) + (lane & (kFeats / 8 - 1));
+    auto read_desc = [&](int64_t f) {
+        if (lane < kFeats / 8 && f + dr < f1) {
+            if (tab) pf = tab[f + dr];
+            pz = S[a.F * a.dv + f + dr];
+        }
+    };
+    auto put_desc = [&](int64_t f, int buf) {
+        if (lane < kFeats / 8) {
+            FeatDesc fd = {};  // weight 0 past the last feature
+            if (f + dr < f1)
+                fd = tab ? desc_from_packed(pf, coef, true) : make_desc(a.d, a.n, f + dr, a.tau, true);
+            uint32_t packed = 0;  // factors past the degree point at the row of ones
+            for (int p = 0; p < kMaxN - 1; ++p)
+                packed |= (p < fd.m ? (fd.packed >> (8 * p)) & 0xffu : (uint32_t)a.d) << (8 * p);
+            code[buf][dr] = packed;
+            weight[buf][dr] = fd.w;
+            zt[buf][dr] = f + dr < f1 ? pz : 0.f;
+        }
+    };
+    const int mq = tid % MB, fg = tid / MB;      // forming features
+    const int mg = tid / 16, cg = tid % 16 * 4;  // multiplying
+    f32x2 acc[TM][2] = {};
+    float z = 0.f;
+    load(f0, 0);
+    read_desc(f0);
+    put_desc(f0, 0);
+    int buf = 0;
+    for (int64_t f = f0; f < f1; f += kFeats, buf ^= 1) {
+        ptx::cp_async_wait<0>();
+        __syncthreads();  // this step's state and descriptors are there, the last step's are free
+        const bool more = f + kFeats < f1;
+        if (more) load(f + kFeats, buf ^ 1), read_desc(f + kFeats);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = fg * PER + i;
+            const uint32_t p = code[buf][r];
+            float v = weight[buf][r];
+            for (int e = 0; e < a.n - 1; ++e) v *= xs[(p >> (8 * e)) & 0xffu][mq];
+            phi[r][mq] = v;
+            z = fmaf(v, zt[buf][r], z);
+        }
+        __syncthreads();
+#pragma unroll 8
+        for (int r = 0; r < kFeats; ++r) {
+            const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(&st[buf][r][cg]);
+            float p[TM];
+            if constexpr (TM == 4) *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(&phi[r][mg * 4]);
+            else if constexpr (TM == 2) *reinterpret_cast<float2*>(p) = *reinterpret_cast<const float2*>(&phi[r][mg * 2]);
+            else p[0] = phi[r][mg];
+#pragma unroll
+            for (int t = 0; t < TM; ++t) {
+                const f32x2 pp = make2(p[t], p[t]);
+                acc[t][0] = fma2(pp, s.x, acc[t][0]);
+                acc[t][1] = fma2(pp, s.y, acc[t][1]);
+            }
+        }
+        if (more) put_desc(f + kFeats, buf ^ 1);
+    }
+    const int pitch = a.dv + 4;
+    float* Y = a.part + ((int64_t)split * a.H + h) * a.B * pitch;
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+        const int m = mg * TM + t;
+        if (m < nq && cg < ncol) {
+            const float2 lo = split2(acc[t][0]), hi = split2(acc[t][1]);
+            *reinterpret_cast<float4*>(Y + (int64_t)(b0 + m) * pitch + c0 + cg) = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+    }
+    if (ct == 0) {
+        __syncthreads();
+        phi[fg][mq] = z;
+        __syncthreads();
+        if (tid < nq) {
+            float v = 0.f;
+            for (int g = 0; g < 256 / MB; ++g) v += phi[g][tid];
+            Y[(int64_t)(b0 + tid) * pitch + a.dv] = v;
+        }
+    }
+}
+
+// ------------------------------------------------------------ the own tokens
+// One cluster of CTAs per sequence and head (one CTA but for long suffixes of
+// few heads).  Eight lanes take a token: each multiplies its share of q and k,
+// three shuffles make the score, and with the weight K(tau q.k) each adds its
+// share of v, so a warp has four tokens a step and U steps in flight; rows are
+// read once, in pieces of up to 16 bytes.  Bound by the cache's bytes.  The
+// sums of the lanes, warps and CTAs and the shared part's shares are joined in
+// an order that depends on the sizes alone.
+constexpr int kUnroll = 4;
+constexpr int kOwnTokens = 32 * kUnroll;  // of a CTA and step
+
+template <typename T, int N>
+struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Span {
+    T v[N];
+};
+template <typename T, int N>
+__device__ __forceinline__ void to_floats(const Span<T, N>& p, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_float(p.v[i]);
+}
+
+__device__ __forceinline__ float load_remote(const float* mine, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(ptx::smem_u32(mine)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// KV: entries of k a lane reads at once (0: one by one, any d_k); VV: columns
+// of v it reads at once, J times.
+template <typename T, int KV, int VV, int J>
+__global__ void __launch_bounds__(256)
+prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster) {
+    constexpr int KE = KV ? KV : kMaxDk / 8;
+    __shared__ __align__(16) float red[8][kMaxDv + 4];
+    __shared__ float tot[kMaxDv + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & 7, grp = lane >> 3;
+    const int rank = blockIdx.x % cluster, bh = blockIdx.x / cluster, b = bh / a.H, h = bh - b * a.H;
     const T* k = static_cast<const T*>(a.k) + (int64_t)bh * a.d;
     const T* v = static_cast<const T*>(a.v) + (int64_t)bh * a.dv;
     T* kc = static_cast<T*>(a.kc) + (int64_t)bh * a.cap * a.d;
     T* vc = static_cast<T*>(a.vc) + (int64_t)bh * a.cap * a.dv;
     const int L = a.lengths[b];
-    if (L < 0 || L >= a.cap) {
-        if (tid < a.dv) a.out[(int64_t)bh * a.dv + tid] = nanf("");
-        if (tid == 0) atomicOr(a.err, kErrLength);
+    if (L < 0 || L >= a.cap) {  // the same in every CTA of the cluster
+        ptx::pdl_wait_primary();
+        if (rank == 0 && tid < a.dv) a.out[(int64_t)bh * a.dv + tid] = nanf("");
+        if (rank == 0 && tid == 0) atomicOr(a.err, kErrLength);
         return;
     }
-    if (tid < a.d) qs[tid] = to_float(q[tid]);
-    if (tid < a.n) coef[tid] = query_coeff(tid, a.tau);
-    __syncthreads();
-    const PackedFeat* tab = feat_table(a.d, a.n);
-    const float* S = a.state + (int64_t)h * a.stride;
-    // thread c sums column c, thread 0 column d_v too
-    float y = 0.f, z = 0.f;
-    for (int64_t f0 = 0; f0 < a.F; f0 += 256) {
-        if (f0 + tid < a.F) phi[tid] = eval_desc(get_desc(tab, a.d, a.n, f0 + tid, a.tau, coef, true), qs);
-        __syncthreads();
-        const int nf = (int)min64(256, a.F - f0);
-        if (tid < a.dv)
-            for (int f = 0; f < nf; ++f) y = fmaf(phi[f], S[(f0 + f) * a.dv + tid], y);
-        if (tid == 0)
-            for (int f = 0; f < nf; ++f) z = fmaf(phi[f], S[a.F * a.dv + f0 + f], z);
-        __syncthreads();
+    float q[KE];
+    if constexpr (KV > 0) {
+        const Span<T, KV> p = *reinterpret_cast<const Span<T, KV>*>(static_cast<const T*>(a.q) + (int64_t)bh * a.d + sub * KV);
+        to_floats<T, KV>(p, q);
+    } else {
+#pragma unroll
+        for (int e = 0; e < KE; ++e)
+            q[e] = sub + 8 * e < a.d ? to_float(static_cast<const T*>(a.q)[(int64_t)bh * a.d + sub + 8 * e]) : 0.f;
     }
-    for (int j0 = 0; j0 <= L; j0 += 256) {
-        const int j = j0 + tid;
-        if (j <= L) {
-            const T* row = j < L ? kc + (int64_t)j * a.d : k;
-            float x = 0.f;
-            for (int i = 0; i < a.d; ++i) x = fmaf(qs[i], to_float(row[i]), x);
-            phi[tid] = taylor_kernel(a.tau * x, a.n);
+    // the series' coefficients tau^m / m!, 0 from degree n on
+    float c1 = a.n > 1 ? query_coeff(1, a.tau) : 0.f, c2 = a.n > 2 ? query_coeff(2, a.tau) : 0.f;
+    float c3 = a.n > 3 ? query_coeff(3, a.tau) : 0.f, c4 = a.n > 4 ? query_coeff(4, a.tau) : 0.f;
+
+    f32x2 y[J][VV / 2] = {};
+    float z = 0.f;
+    for (int j0 = rank * kOwnTokens; j0 <= L; j0 += cluster * kOwnTokens) {
+        Span<T, KE> kr[kUnroll];
+        Span<T, VV> vr[kUnroll][J];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int j = j0 + u * 32 + warp * 4 + grp;
+            const bool in = j <= L;
+            const T* krow = j < L ? kc + (int64_t)j * a.d : k;
+            const T* vrow = j < L ? vc + (int64_t)j * a.dv : v;
+            kr[u] = {};
+            if constexpr (KV > 0) {
+                if (in) kr[u] = *reinterpret_cast<const Span<T, KE>*>(krow + sub * KV);
+            } else {
+#pragma unroll
+                for (int e = 0; e < KE; ++e)
+                    if (in && sub + 8 * e < a.d) kr[u].v[e] = krow[sub + 8 * e];
+            }
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                const int c = (i * 8 + sub) * VV;
+                vr[u][i] = {};
+                if (in && c < a.dv) vr[u][i] = *reinterpret_cast<const Span<T, VV>*>(vrow + c);
+            }
         }
-        __syncthreads();
-        const int nj = min(256, L + 1 - j0);
-        for (int i = 0; i < nj; ++i) {
-            const T* row = j0 + i < L ? vc + (int64_t)(j0 + i) * a.dv : v;
-            if (tid < a.dv) y = fmaf(phi[i], to_float(row[tid]), y);
-            if (tid == 0) z += phi[i];
+        float x[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            float kf[KE];
+            to_floats<T, KE>(kr[u], kf);
+            x[u] = 0.f;
+#pragma unroll
+            for (int e = 0; e < KE; ++e) x[u] = fmaf(q[e], kf[e], x[u]);
         }
-        __syncthreads();
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) x[u] += __shfl_xor_sync(0xffffffffu, x[u], o);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int j = j0 + u * 32 + warp * 4 + grp;
+            float w = fmaf(x[u], fmaf(x[u], fmaf(x[u], fmaf(x[u], c4, c3), c2), c1), 1.f);
+            if (j > L) w = 0.f;
+            z += w;
+            const f32x2 ww = make2(w, w);
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                float vf[VV];
+                to_floats<T, VV>(vr[u][i], vf);
+#pragma unroll
+                for (int e = 0; e < VV / 2; ++e) y[i][e] = fma2(ww, make2(vf[2 * e], vf[2 * e + 1]), y[i][e]);
+            }
+        }
     }
-    if (tid < a.dv) num[tid] = y;
-    if (tid == 0) num[a.dv] = z;
+    // the warp's four token groups
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+        z += __shfl_xor_sync(0xffffffffu, z, o);
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+#pragma unroll
+            for (int e = 0; e < VV / 2; ++e) {
+                float2 f = split2(y[i][e]);
+                f.x += __shfl_xor_sync(0xffffffffu, f.x, o);
+                f.y += __shfl_xor_sync(0xffffffffu, f.y, o);
+                y[i][e] = make2(f.x, f.y);
+            }
+    }
+    if (grp == 0) {
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+#pragma unroll
+            for (int e = 0; e < VV / 2; ++e) {
+                const int c = (i * 8 + sub) * VV + 2 * e;
+                if (c < a.dv) *reinterpret_cast<float2*>(&red[warp][c]) = split2(y[i][e]);
+            }
+        if (sub == 0) red[warp][a.dv] = z;
+    }
+    __syncwarp();
+    if (rank == 0) {  // the shared part's shares, warp by warp
+        ptx::pdl_wait_primary();
+        const int pitch = a.dv + 4;
+        for (int c = lane * 4; c <= a.dv; c += 128) {
+            float4 s = *reinterpret_cast<float4*>(&red[warp][c]);
+            for (int i = warp; i < splits; i += 8) {
+                const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part + (((int64_t)i * a.H + h) * a.B + b) * pitch + c));
+                s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+            }
+            *reinterpret_cast<float4*>(&red[warp][c]) = s;
+        }
+    }
     __syncthreads();
-    if (tid < a.dv) a.out[(int64_t)bh * a.dv + tid] = num[tid] / num[a.dv];
-    if (tid < a.d) kc[(int64_t)L * a.d + tid] = k[tid];
-    if (tid < a.dv) vc[(int64_t)L * a.dv + tid] = v[tid];
+    for (int c = tid; c <= a.dv; c += 256) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) s += red[w][c];
+        tot[c] = s;
+    }
+    if (cluster > 1) {
+        cluster_barrier();
+        if (rank == 0)
+            for (int c = tid; c <= a.dv; c += 256) {
+                float s = tot[c];
+                for (int i = 1; i < cluster; ++i) s += load_remote(&tot[c], i);
+                tot[c] = s;
+            }
+        cluster_barrier();  // the others' sums are read before they leave
+    }
+    __syncthreads();
+    if (rank == 0) {
+        if (tid < a.dv) {
+            a.out[(int64_t)bh * a.dv + tid] = tot[tid] / tot[a.dv];
+            vc[(int64_t)L * a.dv + tid] = v[tid];
+        }
+        if (tid < a.d) kc[(int64_t)L * a.d + tid] = k[tid];
+    }
+}
+
+template <typename T, int KV, int VV>
+void (*own_kernel_j(int dv))(PrefixArgs, int, int) {
+    const int j = (dv + 8 * VV - 1) / (8 * VV);
+    if (j <= 1) return prefix_own_kernel<T, KV, VV, 1>;
+    if (j <= 2) return prefix_own_kernel<T, KV, VV, 2>;
+    if (VV == 8 || j <= 4) return prefix_own_kernel<T, KV, VV, 4>;
+    if constexpr (VV == 4) return prefix_own_kernel<T, KV, 4, 8>;
+    return nullptr;
+}
+template <typename T, int KV>
+void (*own_kernel_v(int dv))(PrefixArgs, int, int) {
+    // 16-byte pieces of v where its rows hold whole ones for all lanes
+    if constexpr (sizeof(T) == 2)
+        if (dv % 64 == 0) return own_kernel_j<T, KV, 8>(dv);
+    return own_kernel_j<T, KV, 4>(dv);
+}
+template <typename T>
+void (*own_kernel(int d, int dv))(PrefixArgs, int, int) {
+    if (d == 64) return own_kernel_v<T, 8>(dv);
+    if (d == 32) return own_kernel_v<T, 4>(dv);
+    if (d == 16) return own_kernel_v<T, 2>(dv);
+    return own_kernel_v<T, 0>(dv);
 }
 
 template <typename T>
 cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
-    TA_TIMED(stream, "prefix_head_kernel", prefix_head_kernel<T><<<(unsigned)(a.B * a.H), 256, 0, stream>>>(a));
-    return cudaGetLastError();
+    const int sms = entry::num_sms();
+    // the shared part: two CTAs an SM, a share of at least 32 features each
+    const int MB = a.B <= 16 ? 16 : a.B <= 32 ? 32 : 64;
+    const int btiles = (a.B + MB - 1) / MB, ctiles = (a.dv + kCols - 1) / kCols;
+    const int64_t tiles = (int64_t)a.H * btiles * ctiles, all = (a.F + kFeats - 1) / kFeats;
+    int64_t splits = 2 * sms / tiles;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    if (splits > all) splits = all;
+    if (splits < 1) splits = 1;
+    const int64_t steps = (all + splits - 1) / splits;
+    splits = (all + steps - 1) / steps;
+    // the own tokens: CTAs of one sequence and head share them while that
+    // leaves each a few steps and the GPU has room
+    const int64_t heads = (int64_t)a.B * a.H;
+    int64_t cluster = (int64_t)sms * 4 / heads, room = ((int64_t)a.cap + 4 * kOwnTokens - 1) / (4 * kOwnTokens);
+    if (cluster > room) cluster = room;
+    if (cluster > 8) cluster = 8;
+    if (cluster < 1) cluster = 1;
+
+    const size_t bytes = (size_t)splits * heads * (a.dv + 4) * sizeof(float);
+    cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&a.part), bytes, stream);
+    if (e != cudaSuccess) return e;
+    auto state = MB == 16 ? prefix_state_kernel<T, 16> : MB == 32 ? prefix_state_kernel<T, 32> : prefix_state_kernel<T, 64>;
+    TA_TIMED(stream, "prefix_state_kernel",
+             state<<<(unsigned)(tiles * splits), 256, 0, stream>>>(a, (int)splits, ctiles, btiles, (int)steps));
+    e = cudaGetLastError();
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(heads * cluster));
+        cfg.blockDim = dim3(256);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)cluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = cluster > 1 ? 2 : 1;
+        TA_TIMED(stream, "prefix_own_kernel",
+                 e = cudaLaunchKernelEx(&cfg, own_kernel<T>(a.d, a.dv), a, (int)splits, (int)cluster));
+    }
+    const cudaError_t f = workspace_free(a.part, stream);
+    return e == cudaSuccess ? f : e;
 }
 
 template <typename T>
@@ -104,7 +437,7 @@ int prefix_entry(const T* q, const T* k, const T* v, const float* state, T* kc, 
                  float* out, int B, int H, int cap, int d, int dv, int n, float tau, cudaStream_t stream) {
     if (B < 0 || H < 0 || cap < 0 || d < 0 || dv < 0 || n < 0 || !isfinite(tau)) return TAYLOR_ERR_INVALID_ARG;
     if (n < 1 || n > kMaxN || d < 1 || d > kMaxDk || dv < 4 || dv > kMaxDv || dv % 4 != 0) return TAYLOR_ERR_UNSUPPORTED;
-    if ((int64_t)B * H >= ((int64_t)1 << 24)) return TAYLOR_ERR_UNSUPPORTED;
+    if ((int64_t)B * H >= ((int64_t)1 << 24) || cap > (1 << 30)) return TAYLOR_ERR_UNSUPPORTED;
     if (B == 0 || H == 0) return TAYLOR_OK;
     if (cap < 1 || !q || !k || !v || !state || !kc || !vc || !lengths || !out) return TAYLOR_ERR_INVALID_ARG;
     const void* p[] = {q, k, v, state, kc, vc, out};

@@ -127,7 +127,7 @@ def test_gated_step_refuses(over, status):
 @pytest.mark.parametrize("over,status", [
     (dict(B=-1), INV), (dict(H=-1), INV), (dict(cap=-1), INV), (dict(cap=0), INV), (dict(tau=float("inf")), INV),
     (dict(n=0), UNS), (dict(n=6), UNS), (dict(d=65), UNS), (dict(d=0), UNS), (dict(dv=62), UNS), (dict(dv=260), UNS),
-    (dict(B=1 << 12, H=1 << 12), UNS), (dict(q=None), INV), (dict(state=None), INV), (dict(kc=None), INV),
+    (dict(B=1 << 12, H=1 << 12), UNS), (dict(cap=(1 << 30) + 1), UNS), (dict(q=None), INV), (dict(state=None), INV), (dict(kc=None), INV),
     (dict(lengths=None), INV), (dict(out=None), INV), (dict(vc=P + 8), MIS), (dict(state=P + 4), MIS),
     (dict(lengths=P + 2), MIS), (dict(B=0, q=None), OK), (dict(H=0, out=None), OK),
 ])
