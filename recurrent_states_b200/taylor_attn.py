@@ -8,7 +8,6 @@ C names; shape arguments (B, H, N, d_k, d_v) are read from the tensors.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -134,17 +133,12 @@ def _need(t: torch.Tensor, name: str, dtype, device=None, shape=None) -> None:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-_HERE = contextlib.nullcontext()
-
-
 def _on(t: torch.Tensor, stream):
     """Context in which t's device is the current one and `stream` (None: that
     device's current stream) its current stream, so that what is allocated in
     it belongs to the stream the kernels run on."""
-    if not t.is_cuda:
-        raise ValueError("the tensors must be CUDA tensors")
     if stream is None:
-        return _HERE if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+        return torch.cuda.device(t.device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = (torch.cuda.ExternalStream(int(stream), device=t.device) if int(stream)
                   else torch.cuda.default_stream(t.device))
@@ -153,18 +147,40 @@ def _on(t: torch.Tensor, stream):
     return torch.cuda.stream(stream)
 
 
-def _rows(t: torch.Tensor, name: str, dtype, device, shape) -> None:
-    """_need for a tensor of any strides whose last dimension is contiguous."""
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call on t has to be made in the context _on(t, stream): another
+    device than the current one, or a stream that was given."""
     if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the tensors must be CUDA tensors")
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
+# The current stream's handle of a device; the public call makes a Stream
+# object first, which takes longer than a small kernel's launch.
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _want(t: torch.Tensor, name: str, dtype, dev: int, shape) -> None:
+    """_need against a device's index; the checks in their quickest form."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _need(t, name, dtype, torch.device("cuda", dev), shape)
+
+
+def _rows(t: torch.Tensor, name: str, dtype, dev: int, shape):
+    """_want for a tensor of any strides whose last dimension is contiguous; returns its strides."""
+    strides = t.stride()
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or (strides[-1] != 1 and shape[-1] > 1):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    return strides
 
 
 # --------------------------------------------------------------- host queries
@@ -394,44 +410,51 @@ def taylor_attn_state_merge(a, b, d_k: int, d_v: int, n: int, out=None, stream=N
     return out
 
 
-def _qk_args(q, k, freqs, positions, q_weight, k_weight, dtype):
+_Three = _I64 * 3
+_Two = _I64 * 2
+
+
+def _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype):
+    """Checks what both directions share: sizes, device, strides of q and k, frequencies."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k must be [B, N, H, d]")
     B, N, Hq, d = q.shape
-    Hk = k.shape[2]
-    _rows(q, "q", dtype, q.device, q.shape)
-    _rows(k, "k", dtype, q.device, (B, N, Hk, d))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, torch.float32, q.device, (d,))
+    Hk, dev = k.size(2), q.get_device()
+    qs = _rows(q, "q", dtype, dev, q.shape)
+    ks = _rows(k, "k", dtype, dev, (B, N, Hk, d))
+    if q_weight is not None:
+        _want(q_weight, "q_weight", torch.float32, dev, (d,))
+    if k_weight is not None:
+        _want(k_weight, "k_weight", torch.float32, dev, (d,))
     if positions is not None:
-        _need(positions, "positions", torch.int64, q.device, (B, N))
+        _want(positions, "positions", torch.int64, dev, (B, N))
     freqs = np.ascontiguousarray(freqs, dtype=np.float64)
     if freqs.ndim != 1:
         raise ValueError("freqs must hold one frequency for each rotated pair")
-    return B, N, Hq, Hk, d, freqs
-
-
-def _strides(t: torch.Tensor):
-    return (_I64 * 3)(*t.stride()[:3])
+    return B, N, Hq, Hk, d, dev, qs, ks, freqs
 
 
 def _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight, interleaved, eps, q_out, k_out,
                   stream):
-    with _on(q, stream):
-        B, N, Hq, Hk, d, freqs = _qk_args(q, k, freqs, positions, q_weight, k_weight, dtype)
-        if q_out is None:
-            q_out = torch.empty((B, Hq, N, d), dtype=dtype, device=q.device)
-        else:
-            _need(q_out, "q_out", dtype, q.device, (B, Hq, N, d))
-        if k_out is None:
-            k_out = torch.empty((B, Hk, N, d), dtype=dtype, device=q.device)
-        else:
-            _need(k_out, "k_out", dtype, q.device, (B, Hk, N, d))
-        rc = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), int(pos0),
-                                  freqs.ctypes.data, 2 * len(freqs), int(bool(interleaved)), _ptr(q_out),
-                                  _ptr(k_out), B, N, Hq, Hk, d, _strides(q), _strides(k), float(eps), _stream(None))
-    _check(rc, name)
+    if _elsewhere(q, stream):
+        with _on(q, stream):
+            return _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight, interleaved, eps,
+                                 q_out, k_out, None)
+    B, N, Hq, Hk, d, dev, qs, ks, freqs = _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype)
+    if q_out is None:
+        q_out = q.new_empty(B, Hq, N, d)
+    else:
+        _want(q_out, "q_out", dtype, dev, (B, Hq, N, d))
+    if k_out is None:
+        k_out = k.new_empty(B, Hk, N, d)
+    else:
+        _want(k_out, "k_out", dtype, dev, (B, Hk, N, d))
+    rc = getattr(lib(), name)(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions), pos0,
+                              freqs.ctypes.data, 2 * len(freqs), bool(interleaved), q_out.data_ptr(),
+                              k_out.data_ptr(), B, N, Hq, Hk, d, _Three(*qs[:3]), _Three(*ks[:3]), eps,
+                              _current(dev))
+    if rc:
+        raise TaylorAttnError(rc, name)
     return q_out, k_out
 
 
@@ -454,25 +477,28 @@ def taylor_attn_qk_norm_rope_f32(q, k, freqs, positions=None, pos0: int = 0, q_w
 
 def _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, pos0, q_weight, k_weight,
                            interleaved, eps, dq, dk, stream):
-    with _on(q, stream):
-        B, N, Hq, Hk, d, freqs = _qk_args(q, k, freqs, positions, q_weight, k_weight, dtype)
-        _need(dq_out, "dq_out", dtype, q.device, (B, Hq, N, d))
-        _need(dk_out, "dk_out", dtype, q.device, (B, Hk, N, d))
-        if dq is None:
-            dq = torch.empty((B, N, Hq, d), dtype=dtype, device=q.device)
-        else:
-            _rows(dq, "dq", dtype, q.device, q.shape)
-        if dk is None:
-            dk = torch.empty((B, N, Hk, d), dtype=dtype, device=q.device)
-        else:
-            _rows(dk, "dk", dtype, q.device, k.shape)
-        dqw = None if q_weight is None else torch.empty_like(q_weight)
-        dkw = None if k_weight is None else torch.empty_like(k_weight)
-        rc = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(q_weight), _ptr(k_weight),
-                                  _ptr(positions), int(pos0), freqs.ctypes.data, 2 * len(freqs),
-                                  int(bool(interleaved)), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), B, N, Hq, Hk, d,
-                                  _strides(q), _strides(k), _strides(dq), _strides(dk), float(eps), _stream(None))
-    _check(rc, name)
+    if _elsewhere(q, stream):
+        with _on(q, stream):
+            return _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, pos0, q_weight,
+                                          k_weight, interleaved, eps, dq, dk, None)
+    B, N, Hq, Hk, d, dev, qs, ks, freqs = _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype)
+    _want(dq_out, "dq_out", dtype, dev, (B, Hq, N, d))
+    _want(dk_out, "dk_out", dtype, dev, (B, Hk, N, d))
+    if dq is None:
+        dq = q.new_empty(B, N, Hq, d)
+    if dk is None:
+        dk = k.new_empty(B, N, Hk, d)
+    dqs = _rows(dq, "dq", dtype, dev, q.shape)
+    dks = _rows(dk, "dk", dtype, dev, k.shape)
+    dqw = None if q_weight is None else torch.empty_like(q_weight)
+    dkw = None if k_weight is None else torch.empty_like(k_weight)
+    rc = getattr(lib(), name)(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), _ptr(q_weight),
+                              _ptr(k_weight), _ptr(positions), pos0, freqs.ctypes.data, 2 * len(freqs),
+                              bool(interleaved), dq.data_ptr(), dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, N, Hq, Hk, d,
+                              _Three(*qs[:3]), _Three(*ks[:3]), _Three(*dqs[:3]), _Three(*dks[:3]), eps,
+                              _current(dev))
+    if rc:
+        raise TaylorAttnError(rc, name)
     return dq, dk, dqw, dkw
 
 
@@ -495,37 +521,37 @@ def taylor_attn_qk_norm_rope_backward_f32(q, k, dq_out, dk_out, freqs, positions
                                   freqs, positions, pos0, q_weight, k_weight, interleaved, eps, dq, dk, stream)
 
 
-def _gated_args(gate, x, h0, lengths, dtype):
+def _gated_sides(gate, x, h0, lengths, dtype):
     if gate.dim() != 3:
         raise ValueError("gate, x must be [B, N, D]")
-    B, N, D = gate.shape
-    _rows(gate, "gate", dtype, gate.device, gate.shape)
-    _rows(x, "x", dtype, gate.device, gate.shape)
+    B, N, D = shape = gate.shape
+    dev = gate.get_device()
+    gs = _rows(gate, "gate", dtype, dev, shape)
+    xs = _rows(x, "x", dtype, dev, shape)
     if h0 is not None:
-        _need(h0, "h0", torch.float32, gate.device, (B, D))
+        _want(h0, "h0", torch.float32, dev, (B, D))
     if lengths is not None:
-        _need(lengths, "lengths", torch.int32, gate.device, (B,))
-    return B, N, D
-
-
-def _two(t: torch.Tensor):
-    return (_I64 * 2)(*t.stride()[:2])
+        _want(lengths, "lengths", torch.int32, dev, (B,))
+    return B, N, D, dev, gs, xs
 
 
 def _gated_scan(name, dtype, gate, x, coupled, h0, lengths, h, h_last, stream):
-    with _on(gate, stream):
-        B, N, D = _gated_args(gate, x, h0, lengths, dtype)
-        if h is None:
-            h = torch.empty((B, N, D), dtype=dtype, device=gate.device)
-        else:
-            _need(h, "h", dtype, gate.device, (B, N, D))
-        if h_last is True:
-            h_last = torch.empty((B, D), dtype=torch.float32, device=gate.device)
-        elif h_last is not None:
-            _need(h_last, "h_last", torch.float32, gate.device, (B, D))
-        rc = getattr(lib(), name)(_ptr(gate), _ptr(x), _ptr(h0), _ptr(lengths), _ptr(h), _ptr(h_last), B, N, D,
-                                  _two(gate), _two(x), int(bool(coupled)), _stream(None))
-    _check(rc, name)
+    if _elsewhere(gate, stream):
+        with _on(gate, stream):
+            return _gated_scan(name, dtype, gate, x, coupled, h0, lengths, h, h_last, None)
+    B, N, D, dev, gs, xs = _gated_sides(gate, x, h0, lengths, dtype)
+    if h is None:
+        h = gate.new_empty(B, N, D)
+    else:
+        _want(h, "h", dtype, dev, (B, N, D))
+    if h_last is True:
+        h_last = torch.empty((B, D), dtype=torch.float32, device=gate.device) if h0 is None else torch.empty_like(h0)
+    elif h_last is not None:
+        _want(h_last, "h_last", torch.float32, dev, (B, D))
+    rc = getattr(lib(), name)(gate.data_ptr(), x.data_ptr(), _ptr(h0), _ptr(lengths), h.data_ptr(), _ptr(h_last), B, N,
+                              D, _Two(*gs[:2]), _Two(*xs[:2]), bool(coupled), _current(dev))
+    if rc:
+        raise TaylorAttnError(rc, name)
     return h, h_last
 
 
@@ -545,30 +571,32 @@ def taylor_attn_gated_scan_f32(gate, x, coupled: bool = True, h0=None, lengths=N
 
 
 def _gated_scan_backward(name, dtype, gate, x, h, dh, coupled, h0, lengths, dh_last, dgate, dx, dh0, stream):
-    with _on(gate, stream):
-        B, N, D = _gated_args(gate, x, h0, lengths, dtype)
-        _need(h, "h", dtype, gate.device, (B, N, D))
-        _need(dh, "dh", dtype, gate.device, (B, N, D))
-        if dh_last is not None:
-            _need(dh_last, "dh_last", torch.float32, gate.device, (B, D))
-        if dgate is None:
-            dgate = torch.empty((B, N, D), dtype=dtype, device=gate.device)
-        else:
-            _rows(dgate, "dgate", dtype, gate.device, (B, N, D))
-        if dx is None:
-            dx = torch.empty((B, N, D), dtype=dtype, device=gate.device)
-        else:
-            _rows(dx, "dx", dtype, gate.device, (B, N, D))
-        if dh0 is True:
-            dh0 = torch.empty((B, D), dtype=torch.float32, device=gate.device)
-        elif dh0 is False:
-            dh0 = None
-        elif dh0 is not None:
-            _need(dh0, "dh0", torch.float32, gate.device, (B, D))
-        rc = getattr(lib(), name)(_ptr(gate), _ptr(x), _ptr(h), _ptr(dh), _ptr(h0), _ptr(lengths), _ptr(dh_last),
-                                  _ptr(dgate), _ptr(dx), _ptr(dh0), B, N, D, _two(gate), _two(x), _two(dgate),
-                                  _two(dx), int(bool(coupled)), _stream(None))
-    _check(rc, name)
+    if _elsewhere(gate, stream):
+        with _on(gate, stream):
+            return _gated_scan_backward(name, dtype, gate, x, h, dh, coupled, h0, lengths, dh_last, dgate, dx, dh0,
+                                        None)
+    B, N, D, dev, gs, xs = _gated_sides(gate, x, h0, lengths, dtype)
+    _want(h, "h", dtype, dev, (B, N, D))
+    _want(dh, "dh", dtype, dev, (B, N, D))
+    if dh_last is not None:
+        _want(dh_last, "dh_last", torch.float32, dev, (B, D))
+    if dgate is None:
+        dgate = torch.empty_like(dh)
+    if dx is None:
+        dx = torch.empty_like(dh)
+    dgs = _rows(dgate, "dgate", dtype, dev, gate.shape)
+    dxs = _rows(dx, "dx", dtype, dev, gate.shape)
+    if dh0 is True:
+        dh0 = torch.empty((B, D), dtype=torch.float32, device=gate.device) if dh_last is None else torch.empty_like(dh_last)
+    elif dh0 is False:
+        dh0 = None
+    elif dh0 is not None:
+        _want(dh0, "dh0", torch.float32, dev, (B, D))
+    rc = getattr(lib(), name)(gate.data_ptr(), x.data_ptr(), h.data_ptr(), dh.data_ptr(), _ptr(h0), _ptr(lengths),
+                              _ptr(dh_last), dgate.data_ptr(), dx.data_ptr(), _ptr(dh0), B, N, D, _Two(*gs[:2]),
+                              _Two(*xs[:2]), _Two(*dgs[:2]), _Two(*dxs[:2]), bool(coupled), _current(dev))
+    if rc:
+        raise TaylorAttnError(rc, name)
     return dgate, dx, dh0
 
 
@@ -590,24 +618,28 @@ def taylor_attn_gated_scan_backward_f32(gate, x, h, dh, coupled: bool = True, h0
 
 
 def _gated_step(name, dtype, gate, x, state, coupled, out, state_out, stream):
-    with _on(gate, stream):
-        if gate.dim() != 2:
-            raise ValueError("gate, x must be [B, D]")
-        B, D = gate.shape
-        _rows(gate, "gate", dtype, gate.device, (B, D))
-        _rows(x, "x", dtype, gate.device, (B, D))
-        _need(state, "state", torch.float32, gate.device, (B, D))
-        if state_out is None:
-            state_out = state
-        else:
-            _need(state_out, "state_out", torch.float32, gate.device, (B, D))
-        if out is None:
-            out = torch.empty((B, D), dtype=dtype, device=gate.device)
-        else:
-            _need(out, "out", dtype, gate.device, (B, D))
-        rc = getattr(lib(), name)(_ptr(gate), _ptr(x), _ptr(state), _ptr(state_out), _ptr(out), B, D, gate.stride(0),
-                                  x.stride(0), int(bool(coupled)), _stream(None))
-    _check(rc, name)
+    if _elsewhere(gate, stream):
+        with _on(gate, stream):
+            return _gated_step(name, dtype, gate, x, state, coupled, out, state_out, None)
+    if gate.dim() != 2:
+        raise ValueError("gate, x must be [B, D]")
+    B, D = shape = gate.shape
+    dev = gate.get_device()
+    gs = _rows(gate, "gate", dtype, dev, shape)
+    xs = _rows(x, "x", dtype, dev, shape)
+    _want(state, "state", torch.float32, dev, shape)
+    if state_out is None:
+        state_out = state
+    else:
+        _want(state_out, "state_out", torch.float32, dev, shape)
+    if out is None:
+        out = gate.new_empty(B, D)
+    else:
+        _want(out, "out", dtype, dev, shape)
+    rc = getattr(lib(), name)(gate.data_ptr(), x.data_ptr(), state.data_ptr(), state_out.data_ptr(), out.data_ptr(), B,
+                              D, gs[0], xs[0], bool(coupled), _current(dev))
+    if rc:
+        raise TaylorAttnError(rc, name)
     return out
 
 
@@ -624,29 +656,33 @@ def taylor_attn_gated_step_f32(gate, x, state, coupled: bool = True, out=None, s
 
 
 def _shared_prefix_decode(name, dtype, q, k, v, prefix_state, k_cache, v_cache, lengths, n, tau, out, stream):
-    with _on(q, stream):
-        if q.dim() != 3 or k_cache.dim() != 4:
-            raise ValueError("q, k must be [B, H, d_k], v [B, H, d_v] and the caches [B, H, cap, d]")
-        B, H, d_k = q.shape
-        d_v, cap = v.shape[-1], k_cache.shape[2]
-        stride = taylor_attn_state_stride(d_k, d_v, n)
-        if stride < 0:
-            raise TaylorAttnError(TAYLOR_ERR_UNSUPPORTED, name)
-        _need(q, "q", dtype, q.device)
-        _need(k, "k", dtype, q.device, (B, H, d_k))
-        _need(v, "v", dtype, q.device, (B, H, d_v))
-        lead = (1, H) if prefix_state.dim() == 3 else (H,)
-        _need(prefix_state, "prefix_state", torch.float32, q.device, lead + (stride,))
-        _need(k_cache, "k_cache", dtype, q.device, (B, H, cap, d_k))
-        _need(v_cache, "v_cache", dtype, q.device, (B, H, cap, d_v))
-        _need(lengths, "lengths", torch.int32, q.device, (B,))
-        if out is None:
-            out = torch.empty((B, H, d_v), dtype=torch.float32, device=q.device)
-        else:
-            _need(out, "out", torch.float32, q.device, (B, H, d_v))
-        rc = getattr(lib(), name)(_ptr(q), _ptr(k), _ptr(v), _ptr(prefix_state), _ptr(k_cache), _ptr(v_cache),
-                                  _ptr(lengths), _ptr(out), B, H, cap, d_k, d_v, n, float(tau), _stream(None))
-    _check(rc, name)
+    if _elsewhere(q, stream):
+        with _on(q, stream):
+            return _shared_prefix_decode(name, dtype, q, k, v, prefix_state, k_cache, v_cache, lengths, n, tau, out,
+                                         None)
+    if q.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q, k must be [B, H, d_k], v [B, H, d_v] and the caches [B, H, cap, d]")
+    B, H, d_k = q.shape
+    d_v, cap, dev = v.size(-1), k_cache.size(2), q.get_device()
+    stride = lib().taylor_attn_state_stride(d_k, d_v, n)
+    if stride < 0:
+        raise TaylorAttnError(TAYLOR_ERR_UNSUPPORTED, name)
+    _want(q, "q", dtype, dev, q.shape)
+    _want(k, "k", dtype, dev, q.shape)
+    _want(v, "v", dtype, dev, (B, H, d_v))
+    _want(prefix_state, "prefix_state", torch.float32, dev, (1, H, stride) if prefix_state.dim() == 3 else (H, stride))
+    _want(k_cache, "k_cache", dtype, dev, (B, H, cap, d_k))
+    _want(v_cache, "v_cache", dtype, dev, (B, H, cap, d_v))
+    _want(lengths, "lengths", torch.int32, dev, (B,))
+    if out is None:
+        out = torch.empty((B, H, d_v), dtype=torch.float32, device=q.device)
+    else:
+        _want(out, "out", torch.float32, dev, (B, H, d_v))
+    rc = getattr(lib(), name)(q.data_ptr(), k.data_ptr(), v.data_ptr(), prefix_state.data_ptr(), k_cache.data_ptr(),
+                              v_cache.data_ptr(), lengths.data_ptr(), out.data_ptr(), B, H, cap, d_k, d_v, n, tau,
+                              _current(dev))
+    if rc:
+        raise TaylorAttnError(rc, name)
     return out
 
 
