@@ -12,6 +12,8 @@
 // its own.  The new k and v are appended to the cache in the same call.
 #include <math.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "entry.h"
 #include "feature_table.cuh"
@@ -39,6 +41,9 @@ struct PrefixArgs {
     float tau;
 };
 
+#ifndef PREFIX_FILL
+#define PREFIX_FILL 2
+#endif
 // ------------------------------------------------------------ the shared part
 // Y = (c (.) Phi(Q)) S for one head: a product of [queries x F] by [F x d_v],
 // its left side formed feature by feature from q.  A CTA takes MB queries, 64
@@ -49,17 +54,28 @@ struct PrefixArgs {
 // (2 B F (d_v + 1) flops a head against the cache's bytes).
 constexpr int kFeats = 32;    // features a step
 constexpr int kCols = 64;     // columns a CTA
+constexpr int kSteps = 5;     // steps of the state in shared memory, four of them on their way
 
-template <typename T, int MB>
+template <typename T, int N>
+struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Span {
+    T v[N];
+};
+template <typename T, int N>
+__device__ __forceinline__ void to_floats(const Span<T, N>& p, float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = to_float(p.v[i]);
+}
+
+template <typename T, int MB, int NF>
 __global__ void __launch_bounds__(256)
 prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles, int btiles, int steps) {
     constexpr int TM = MB / 16, PER = kFeats * MB / 256;  // queries of a thread; features it forms a step
-    __shared__ __align__(16) float xs[kMaxDk + 1][MB];    // q by entry, row d is 1 (a missing factor)
-    __shared__ __align__(16) float st[2][kFeats][kCols];
-    __shared__ float zt[2][kFeats];
+    extern __shared__ __align__(16) float dyn[];
+    float(*st)[kFeats][kCols] = reinterpret_cast<float(*)[kFeats][kCols]>(dyn);  // [kSteps]
+    float(*zt)[kFeats] = reinterpret_cast<float(*)[kFeats]>(dyn + kSteps * kFeats * kCols);
+    float(*xs)[MB] = reinterpret_cast<float(*)[MB]>(dyn + kSteps * kFeats * (kCols + 1));  // q by entry, row d is 1
     __shared__ __align__(16) float phi[kFeats][MB];
-    __shared__ uint32_t code[2][kFeats];
-    __shared__ float weight[2][kFeats];
+    __shared__ uint2 desc[256];  // factors (8 bits each) and weight of eight steps' features
     __shared__ float coef[kMaxN];
     ptx::pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -75,65 +91,79 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
     const float* S = a.state + (int64_t)h * a.stride;
     const PackedFeat* tab = feat_table(a.d, a.n);
 
-    if (tid < a.n) coef[tid] = query_coeff(tid, a.tau);
-    for (int i = tid; i < MB * a.d; i += 256) {
-        const int m = i / a.d, e = i - m * a.d;
-        xs[e][m] = m < nq ? to_float(static_cast<const T*>(a.q)[((int64_t)(b0 + m) * a.H + h) * a.d + e]) : 0.f;
-    }
-    for (int m = tid; m < MB; m += 256) xs[a.d][m] = 1.f;
-    __syncthreads();
-    auto load = [&](int64_t f, int buf) {  // features f .. f + 31 of the state; past f1: zeros
-        for (int i = tid; i < kFeats * (kCols / 4); i += 256) {
-            const int r = i / (kCols / 4), c = i % (kCols / 4) * 4;
-            const bool in = f + r < f1 && c < ncol;
-            ptx::cp_async16(&st[buf][r][c], in ? S + (f + r) * a.dv + c0 + c : S, in ? 16 : 0);
+    auto load = [&](int64_t step) {  // 32 features of the state and of its column d_v; past f1: zeros
+        const int64_t f = f0 + step * kFeats;
+        const int buf = (int)(step % kSteps);
+        if (f < f1) {
+            for (int i = tid; i < kFeats * (kCols / 4); i += 256) {
+                const int r = i / (kCols / 4), c = i % (kCols / 4) * 4;
+                const bool in = f + r < f1 && c < ncol;
+                ptx::cp_async16(&st[buf][r][c], in ? S + (f + r) * a.dv + c0 + c : S, in ? 16 : 0);
+            }
+            if (tid < kFeats / 4) {
+                const int64_t left = f1 - f - tid * 4;
+                const bool in = left > 0;
+                ptx::cp_async16(&zt[buf][tid * 4], in ? S + a.F * a.dv + f + tid * 4 : S,
+                                in ? (uint32_t)min64(left, 4) * 4 : 0);
+            }
         }
         ptx::cp_async_commit();
     };
-    // a step's descriptors, four a warp: read ahead into registers, put in place later
-    PackedFeat pf = {};
-    float pz = 0.f;
-    const int dr = warp * (kFeats / 8) + (lane & (kFeats / 8 - 1));
-    auto read_desc = [&](int64_t f) {
-        if (lane < kFeats / 8 && f + dr < f1) {
-            if (tab) pf = tab[f + dr];
-            pz = S[a.F * a.dv + f + dr];
+    for (int i = 0; i < kSteps - 1; ++i) load(i);
+    if (tid < a.n) coef[tid] = query_coeff(tid, a.tau);
+    if (a.d * sizeof(T) % 16 == 0) {
+        constexpr int E = 16 / sizeof(T);
+        const int per = a.d / E;
+        for (int i = tid; i < MB * per; i += 256) {
+            const int m = i % MB, e = i / MB * E;
+            Span<T, E> p = {};
+            if (m < nq) p = *reinterpret_cast<const Span<T, E>*>(static_cast<const T*>(a.q) + ((int64_t)(b0 + m) * a.H + h) * a.d + e);
+#pragma unroll
+            for (int j = 0; j < E; ++j) xs[e + j][m] = to_float(p.v[j]);
         }
-    };
-    auto put_desc = [&](int64_t f, int buf) {
-        if (lane < kFeats / 8) {
-            FeatDesc fd = {};  // weight 0 past the last feature
-            if (f + dr < f1)
-                fd = tab ? desc_from_packed(pf, coef, true) : make_desc(a.d, a.n, f + dr, a.tau, true);
-            uint32_t packed = 0;  // factors past the degree point at the row of ones
-            for (int p = 0; p < kMaxN - 1; ++p)
-                packed |= (p < fd.m ? (fd.packed >> (8 * p)) & 0xffu : (uint32_t)a.d) << (8 * p);
-            code[buf][dr] = packed;
-            weight[buf][dr] = fd.w;
-            zt[buf][dr] = f + dr < f1 ? pz : 0.f;
+    } else {
+        for (int i = tid; i < MB * a.d; i += 256) {
+            const int m = i % MB, e = i / MB;
+            xs[e][m] = m < nq ? to_float(static_cast<const T*>(a.q)[((int64_t)(b0 + m) * a.H + h) * a.d + e]) : 0.f;
         }
+    }
+    for (int m = tid; m < MB; m += 256) xs[a.d][m] = 1.f;
+    __syncthreads();
+    auto describe = [&](int64_t f) {  // feature f, one a thread
+        FeatDesc fd = {};  // weight 0 past the last feature
+        if (f < f1) fd = get_desc(tab, a.d, a.n, f, a.tau, coef, true);
+        uint32_t packed = 0;  // factors past the degree point at the row of ones
+#pragma unroll
+        for (int p = 0; p < kMaxN - 1; ++p)
+            packed |= (p < fd.m ? (fd.packed >> (8 * p)) & 0xffu : (uint32_t)a.d) << (8 * p);
+        desc[tid] = make_uint2(packed, __float_as_uint(fd.w));
     };
     const int mq = tid % MB, fg = tid / MB;      // forming features
     const int mg = tid / 16, cg = tid % 16 * 4;  // multiplying
     f32x2 acc[TM][2] = {};
     float z = 0.f;
-    load(f0, 0);
-    read_desc(f0);
-    put_desc(f0, 0);
-    int buf = 0;
-    for (int64_t f = f0; f < f1; f += kFeats, buf ^= 1) {
-        ptx::cp_async_wait<0>();
+    describe(f0 + tid);
+    int64_t step = 0;
+    for (int64_t f = f0; f < f1; f += kFeats, ++step) {
+        const int buf = (int)(step % kSteps), group = (int)(step & 7) * kFeats;
+        ptx::cp_async_wait<kSteps - 2>();
         __syncthreads();  // this step's state and descriptors are there, the last step's are free
-        const bool more = f + kFeats < f1;
-        if (more) load(f + kFeats, buf ^ 1), read_desc(f + kFeats);
+        load(step + kSteps - 1);
+        float val[PER];
+        uint2 ds[PER];
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int r = fg * PER + i;
-            const uint32_t p = code[buf][r];
-            float v = weight[buf][r];
-            for (int e = 0; e < a.n - 1; ++e) v *= xs[(p >> (8 * e)) & 0xffu][mq];
-            phi[r][mq] = v;
-            z = fmaf(v, zt[buf][r], z);
+            ds[i] = desc[group + fg * PER + i];
+            val[i] = __uint_as_float(ds[i].y);
+        }
+#pragma unroll
+        for (int e = 0; e < NF; ++e)
+#pragma unroll
+            for (int i = 0; i < PER; ++i) val[i] *= xs[(ds[i].x >> (8 * e)) & 0xffu][mq];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            phi[fg * PER + i][mq] = val[i];
+            z = fmaf(val[i], zt[buf][fg * PER + i], z);
         }
         __syncthreads();
 #pragma unroll 8
@@ -150,7 +180,7 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
                 acc[t][1] = fma2(pp, s.y, acc[t][1]);
             }
         }
-        if (more) put_desc(f + kFeats, buf ^ 1);
+        if (group == 7 * kFeats && f + kFeats < f1) describe(f + kFeats + tid);
     }
     const int pitch = a.dv + 4;
     float* Y = a.part + ((int64_t)split * a.H + h) * a.B * pitch;
@@ -182,17 +212,41 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
 // read once, in pieces of up to 16 bytes.  Bound by the cache's bytes.  The
 // sums of the lanes, warps and CTAs and the shared part's shares are joined in
 // an order that depends on the sizes alone.
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 2;                // tokens of eight lanes in a step
 constexpr int kOwnTokens = 32 * kUnroll;  // of a CTA and step
 
+// Bytes of a token that one lane keeps in shared memory, and the steps that
+// fit into 64 KB a CTA (two at least).
+template <typename T, int KV, int VV, int J>
+constexpr int kLaneBytes = (KV + J * VV) * (int)sizeof(T);
+template <typename T, int KV, int VV, int J>
+constexpr int kAhead = 65536 / (256 * kUnroll * kLaneBytes<T, KV, VV, J>) < 2   ? 2
+                       : 65536 / (256 * kUnroll * kLaneBytes<T, KV, VV, J>) > 4 ? 4
+                                                                                 : 65536 / (256 * kUnroll * kLaneBytes<T, KV, VV, J>);
+
 template <typename T, int N>
-struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Span {
-    T v[N];
-};
-template <typename T, int N>
-__device__ __forceinline__ void to_floats(const Span<T, N>& p, float (&x)[N]) {
+__device__ __forceinline__ void to_pairs(const Span<T, N>& p, f32x2 (&x)[N / 2]) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_float(p.v[i]);
+        for (int i = 0; i < N / 2; ++i) x[i] = make2(p.v[2 * i], p.v[2 * i + 1]);
+    } else {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) x[i] = make2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    }
+}
+template <int BYTES>
+__device__ __forceinline__ void fetch_async(void* dst, const void* src) {
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+        for (int i = 0; i < BYTES; i += 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(static_cast<char*>(dst) + i)),
+                         "l"(static_cast<const char*>(src) + i)
+                         : "memory");
+    } else {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ptx::smem_u32(dst)), "l"(src), "n"(BYTES)
+                     : "memory");
+    }
 }
 
 __device__ __forceinline__ float load_remote(const float* mine, int rank) {
@@ -210,9 +264,10 @@ __device__ __forceinline__ void cluster_barrier() {
 // KV: entries of k a lane reads at once (0: one by one, any d_k); VV: columns
 // of v it reads at once, J times.
 template <typename T, int KV, int VV, int J>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, J* VV <= 16 ? 3 : 1)
 prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster) {
     constexpr int KE = KV ? KV : kMaxDk / 8;
+    extern __shared__ __align__(16) unsigned char ring[];
     __shared__ __align__(16) float red[8][kMaxDv + 4];
     __shared__ float tot[kMaxDv + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & 7, grp = lane >> 3;
@@ -228,14 +283,19 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
         if (rank == 0 && tid == 0) atomicOr(a.err, kErrLength);
         return;
     }
-    float q[KE];
-    if constexpr (KV > 0) {
-        const Span<T, KV> p = *reinterpret_cast<const Span<T, KV>*>(static_cast<const T*>(a.q) + (int64_t)bh * a.d + sub * KV);
-        to_floats<T, KV>(p, q);
-    } else {
+    f32x2 q[KE / 2];
+    {
+        float qf[KE];
+        if constexpr (KV > 0) {
+            const Span<T, KV> p = *reinterpret_cast<const Span<T, KV>*>(static_cast<const T*>(a.q) + (int64_t)bh * a.d + sub * KV);
+            to_floats<T, KV>(p, qf);
+        } else {
 #pragma unroll
-        for (int e = 0; e < KE; ++e)
-            q[e] = sub + 8 * e < a.d ? to_float(static_cast<const T*>(a.q)[(int64_t)bh * a.d + sub + 8 * e]) : 0.f;
+            for (int e = 0; e < KE; ++e)
+                qf[e] = sub + 8 * e < a.d ? to_float(static_cast<const T*>(a.q)[(int64_t)bh * a.d + sub + 8 * e]) : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < KE / 2; ++e) q[e] = make2(qf[2 * e], qf[2 * e + 1]);
     }
     // the series' coefficients tau^m / m!, 0 from degree n on
     float c1 = a.n > 1 ? query_coeff(1, a.tau) : 0.f, c2 = a.n > 2 ? query_coeff(2, a.tau) : 0.f;
@@ -243,38 +303,80 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
 
     f32x2 y[J][VV / 2] = {};
     float z = 0.f;
-    for (int j0 = rank * kOwnTokens; j0 <= L; j0 += cluster * kOwnTokens) {
+    // tokens ahead, each lane's share in slots that it alone reads
+    constexpr int A = kAhead<T, KV, VV, J>;
+    Span<T, VV>* vring = reinterpret_cast<Span<T, VV>*>(ring);                                  // [A][kUnroll][J][256]
+    Span<T, KE>* kring = reinterpret_cast<Span<T, KE>*>(vring + A * kUnroll * J * 256);         // [A][kUnroll][256]
+    const int stride = cluster * kOwnTokens, mine = warp * 4 + grp, start = rank * kOwnTokens;
+    // rows of the next step to fetch
+    const T* kp = kc + (int64_t)(start + mine) * a.d + sub * KV;
+    const T* vp = vc + (int64_t)(start + mine) * a.dv + sub * VV;
+    int jf = start;
+    const int64_t kstep = (int64_t)stride * a.d, vstep = (int64_t)stride * a.dv;
+    const int ku = 32 * a.d, vu = 32 * a.dv;
+    const bool wide = J * 8 * VV == a.dv;  // every lane's columns exist
+    auto fetch = [&](int slot) {
+        Span<T, KE>* kt = &kring[slot * kUnroll * 256 + tid];
+        Span<T, VV>* vt = &vring[slot * kUnroll * J * 256 + tid];
+        if (jf + kOwnTokens <= L && wide) {  // a whole step of cached tokens
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if constexpr (KV > 0) fetch_async<KV * sizeof(T)>(kt + u * 256, kp + u * ku);
+#pragma unroll
+                for (int i = 0; i < J; ++i) fetch_async<VV * sizeof(T)>(vt + (u * J + i) * 256, vp + u * vu + i * 8 * VV);
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const int j = jf + u * 32 + mine;
+                if (j <= L) {  // the new token comes from k and v
+                    if constexpr (KV > 0) fetch_async<KV * sizeof(T)>(kt + u * 256, j < L ? kp + u * ku : k + sub * KV);
+#pragma unroll
+                    for (int i = 0; i < J; ++i) {
+                        const int c = (i * 8 + sub) * VV;
+                        if (c < a.dv)
+                            fetch_async<VV * sizeof(T)>(vt + (u * J + i) * 256, j < L ? vp + u * vu + i * 8 * VV : v + c);
+                    }
+                }
+            }
+        }
+        ptx::cp_async_commit();
+        jf += stride;
+        kp += kstep;
+        vp += vstep;
+    };
+    auto consume = [&](auto whole, int j0, int slot) {
         Span<T, KE> kr[kUnroll];
         Span<T, VV> vr[kUnroll][J];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int j = j0 + u * 32 + warp * 4 + grp;
-            const bool in = j <= L;
-            const T* krow = j < L ? kc + (int64_t)j * a.d : k;
-            const T* vrow = j < L ? vc + (int64_t)j * a.dv : v;
+            const int j = j0 + u * 32 + mine;
+            const bool in = whole || j <= L;
             kr[u] = {};
             if constexpr (KV > 0) {
-                if (in) kr[u] = *reinterpret_cast<const Span<T, KE>*>(krow + sub * KV);
+                if (in) kr[u] = kring[(slot * kUnroll + u) * 256 + tid];
             } else {
+                const T* krow = j < L ? kc + (int64_t)j * a.d : k;
 #pragma unroll
                 for (int e = 0; e < KE; ++e)
                     if (in && sub + 8 * e < a.d) kr[u].v[e] = krow[sub + 8 * e];
             }
 #pragma unroll
             for (int i = 0; i < J; ++i) {
-                const int c = (i * 8 + sub) * VV;
                 vr[u][i] = {};
-                if (in && c < a.dv) vr[u][i] = *reinterpret_cast<const Span<T, VV>*>(vrow + c);
+                if (whole || (in && (i * 8 + sub) * VV < a.dv)) vr[u][i] = vring[((slot * kUnroll + u) * J + i) * 256 + tid];
             }
         }
         float x[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            float kf[KE];
-            to_floats<T, KE>(kr[u], kf);
-            x[u] = 0.f;
+            f32x2 kf[KE / 2], dot;
+            to_pairs<T, KE>(kr[u], kf);
+            dot = mul2(q[0], kf[0]);
 #pragma unroll
-            for (int e = 0; e < KE; ++e) x[u] = fmaf(q[e], kf[e], x[u]);
+            for (int e = 1; e < KE / 2; ++e) dot = fma2(q[e], kf[e], dot);
+            const float2 f = split2(dot);
+            x[u] = f.x + f.y;
         }
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1)
@@ -282,19 +384,29 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
             for (int u = 0; u < kUnroll; ++u) x[u] += __shfl_xor_sync(0xffffffffu, x[u], o);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int j = j0 + u * 32 + warp * 4 + grp;
             float w = fmaf(x[u], fmaf(x[u], fmaf(x[u], fmaf(x[u], c4, c3), c2), c1), 1.f);
-            if (j > L) w = 0.f;
+            if (!whole && j0 + u * 32 + mine > L) w = 0.f;
             z += w;
             const f32x2 ww = make2(w, w);
 #pragma unroll
             for (int i = 0; i < J; ++i) {
-                float vf[VV];
-                to_floats<T, VV>(vr[u][i], vf);
+                f32x2 vf[VV / 2];
+                to_pairs<T, VV>(vr[u][i], vf);
 #pragma unroll
-                for (int e = 0; e < VV / 2; ++e) y[i][e] = fma2(ww, make2(vf[2 * e], vf[2 * e + 1]), y[i][e]);
+                for (int e = 0; e < VV / 2; ++e) y[i][e] = fma2(ww, vf[e], y[i][e]);
             }
         }
+    };
+#pragma unroll 1
+    for (int i = 0; i < A - 1; ++i) fetch(i);
+    int slot = 0;
+#pragma unroll 1
+    for (int j0 = start; j0 <= L; j0 += stride) {
+        fetch(slot == 0 ? A - 1 : slot - 1);
+        ptx::cp_async_wait<A - 1>();
+        if (j0 + kOwnTokens <= L && wide) consume(std::true_type{}, j0, slot);
+        else consume(std::false_type{}, j0, slot);
+        if (++slot == A) slot = 0;
     }
     // the warp's four token groups
 #pragma unroll
@@ -360,28 +472,51 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
     }
 }
 
+struct OwnKernel {
+    void (*run)(PrefixArgs, int, int);
+    int smem;
+};
+template <typename T, int KV, int VV, int J>
+OwnKernel own_of() {
+    return {prefix_own_kernel<T, KV, VV, J>, 256 * kUnroll * kAhead<T, KV, VV, J> * kLaneBytes<T, KV, VV, J>};
+}
 template <typename T, int KV, int VV>
-void (*own_kernel_j(int dv))(PrefixArgs, int, int) {
+OwnKernel own_kernel_j(int dv) {
     const int j = (dv + 8 * VV - 1) / (8 * VV);
-    if (j <= 1) return prefix_own_kernel<T, KV, VV, 1>;
-    if (j <= 2) return prefix_own_kernel<T, KV, VV, 2>;
-    if (VV == 8 || j <= 4) return prefix_own_kernel<T, KV, VV, 4>;
-    if constexpr (VV == 4) return prefix_own_kernel<T, KV, 4, 8>;
-    return nullptr;
+    if (j <= 1) return own_of<T, KV, VV, 1>();
+    if (j <= 2) return own_of<T, KV, VV, 2>();
+    if constexpr (VV == 4)
+        if (j > 4) return own_of<T, KV, 4, 8>();
+    return own_of<T, KV, VV, 4>();
 }
 template <typename T, int KV>
-void (*own_kernel_v(int dv))(PrefixArgs, int, int) {
+OwnKernel own_kernel_v(int dv) {
     // 16-byte pieces of v where its rows hold whole ones for all lanes
     if constexpr (sizeof(T) == 2)
         if (dv % 64 == 0) return own_kernel_j<T, KV, 8>(dv);
     return own_kernel_j<T, KV, 4>(dv);
 }
 template <typename T>
-void (*own_kernel(int d, int dv))(PrefixArgs, int, int) {
+OwnKernel own_kernel(int d, int dv) {
     if (d == 64) return own_kernel_v<T, 8>(dv);
     if (d == 32) return own_kernel_v<T, 4>(dv);
     if (d == 16) return own_kernel_v<T, 2>(dv);
     return own_kernel_v<T, 0>(dv);
+}
+
+template <typename T, int MB>
+auto state_kernel_n(int n) {
+    switch (n) {
+        case 1: return prefix_state_kernel<T, MB, 0>;
+        case 2: return prefix_state_kernel<T, MB, 1>;
+        case 3: return prefix_state_kernel<T, MB, 2>;
+        case 4: return prefix_state_kernel<T, MB, 3>;
+        default: return prefix_state_kernel<T, MB, 4>;
+    }
+}
+template <typename T>
+auto state_kernel(int MB, int n) {
+    return MB == 16 ? state_kernel_n<T, 16>(n) : MB == 32 ? state_kernel_n<T, 32>(n) : state_kernel_n<T, 64>(n);
 }
 
 template <typename T>
@@ -391,7 +526,7 @@ cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
     const int MB = a.B <= 16 ? 16 : a.B <= 32 ? 32 : 64;
     const int btiles = (a.B + MB - 1) / MB, ctiles = (a.dv + kCols - 1) / kCols;
     const int64_t tiles = (int64_t)a.H * btiles * ctiles, all = (a.F + kFeats - 1) / kFeats;
-    int64_t splits = 2 * sms / tiles;
+    int64_t splits = PREFIX_FILL * sms / tiles;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits > all) splits = all;
     if (splits < 1) splits = 1;
@@ -408,14 +543,22 @@ cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
     const size_t bytes = (size_t)splits * heads * (a.dv + 4) * sizeof(float);
     cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&a.part), bytes, stream);
     if (e != cudaSuccess) return e;
-    auto state = MB == 16 ? prefix_state_kernel<T, 16> : MB == 32 ? prefix_state_kernel<T, 32> : prefix_state_kernel<T, 64>;
+    const auto state = state_kernel<T>(MB, a.n);
+    const size_t smem = (size_t)(kSteps * kFeats * (kCols + 1) + (a.d + 1) * MB) * sizeof(float);
+    const OwnKernel own = own_kernel<T>(a.d, a.dv);
+    if ((e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(own.run, cudaFuncAttributeMaxDynamicSharedMemorySize, own.smem)) != cudaSuccess) {
+        workspace_free(a.part, stream);
+        return e;
+    }
     TA_TIMED(stream, "prefix_state_kernel",
-             state<<<(unsigned)(tiles * splits), 256, 0, stream>>>(a, (int)splits, ctiles, btiles, (int)steps));
+             state<<<(unsigned)(tiles * splits), 256, smem, stream>>>(a, (int)splits, ctiles, btiles, (int)steps));
     e = cudaGetLastError();
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(heads * cluster));
         cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = own.smem;
         cfg.stream = stream;
         cudaLaunchAttribute attr[2];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -426,7 +569,7 @@ cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
         cfg.attrs = attr;
         cfg.numAttrs = cluster > 1 ? 2 : 1;
         TA_TIMED(stream, "prefix_own_kernel",
-                 e = cudaLaunchKernelEx(&cfg, own_kernel<T>(a.d, a.dv), a, (int)splits, (int)cluster));
+                 e = cudaLaunchKernelEx(&cfg, own.run, a, (int)splits, (int)cluster));
     }
     const cudaError_t f = workspace_free(a.part, stream);
     return e == cudaSuccess ? f : e;
