@@ -41,20 +41,23 @@ struct PrefixArgs {
     float tau;
 };
 
-#ifndef PREFIX_FILL
-#define PREFIX_FILL 2
-#endif
 // ------------------------------------------------------------ the shared part
-// Y = (c (.) Phi(Q)) S for one head: a product of [queries x F] by [F x d_v],
+// Y = (c (.) Phi(Q)) S for one head: a product of [queries x F] by [F x d_v + 1],
 // its left side formed feature by feature from q.  A CTA takes MB queries, 64
-// columns and a share of the features, 32 at a time; the shares' sums go to
-// the workspace and are joined by the kernel below.  The column d_v of ones
-// (the normaliser) is summed by the threads that form the features.  fp32 FMA
-// throughout: outputs are fp32, and the product is a small part of the call
-// (2 B F (d_v + 1) flops a head against the cache's bytes).
-constexpr int kFeats = 32;    // features a step
+// columns (and z, the column of ones) and a share of the features, 64 a step;
+// the shares' sums go to the workspace and are joined by the kernel below.
+//
+// Outputs are fp32 and the numerator's terms cancel, so the product has to be
+// one of fp32: both sides are split into two tf32 parts, x = hi + lo, and
+// hi hi + hi lo + lo hi goes to the tensor cores (m16n8k8), 22 bits a factor,
+// fp32 sums.  A warp has 16 queries and every n-th group of eight features; it
+// forms its part of Phi in the registers that the instruction reads, each
+// feature once.  On FMA units the operands' way through shared memory bound
+// it: 4 x 4 outputs a thread took 2.2 to 3 us a step of 32 features.
+constexpr int kFeats = 64;    // features a step
 constexpr int kCols = 64;     // columns a CTA
-constexpr int kSteps = 5;     // steps of the state in shared memory, four of them on their way
+constexpr int kPitch = 72;    // floats of a feature's row: the columns, z, zeros; 8 k + n covers the banks
+constexpr int kSteps = 3;     // steps of the state in shared memory, two of them on their way
 
 template <typename T, int N>
 struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Span {
@@ -66,16 +69,28 @@ __device__ __forceinline__ void to_floats(const Span<T, N>& p, float (&x)[N]) {
     for (int i = 0; i < N; ++i) x[i] = to_float(p.v[i]);
 }
 
+// x = hi + lo, hi the upper 11 significant bits (which the tensor cores take
+// as they are; of lo they take as many).
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
 template <typename T, int MB, int NF>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles, int btiles, int steps) {
-    constexpr int TM = MB / 16, PER = kFeats * MB / 256;  // queries of a thread; features it forms a step
+    constexpr int MT = MB / 16, KS = 8 / MT, SLICES = kFeats / 8 / KS;  // query tiles; warps of one; slices of a step
+    constexpr int NT = kPitch / 8, XP = MB + 8;
     extern __shared__ __align__(16) float dyn[];
-    float(*st)[kFeats][kCols] = reinterpret_cast<float(*)[kFeats][kCols]>(dyn);  // [kSteps]
-    float(*zt)[kFeats] = reinterpret_cast<float(*)[kFeats]>(dyn + kSteps * kFeats * kCols);
-    float(*xs)[MB] = reinterpret_cast<float(*)[MB]>(dyn + kSteps * kFeats * (kCols + 1));  // q by entry, row d is 1
-    __shared__ __align__(16) float phi[kFeats][MB];
-    __shared__ uint2 desc[256];  // factors (8 bits each) and weight of eight steps' features
+    float(*st)[kFeats][kPitch] = reinterpret_cast<float(*)[kFeats][kPitch]>(dyn);  // [kSteps]
+    float(*xs)[XP] = reinterpret_cast<float(*)[XP]>(dyn + kSteps * kFeats * kPitch);  // q by entry, row d is 1
+    __shared__ uint2 desc[256];  // factors (8 bits each) and weight of four steps' features
     __shared__ float coef[kMaxN];
     ptx::pdl_launch_dependents();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -91,25 +106,30 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
     const float* S = a.state + (int64_t)h * a.stride;
     const PackedFeat* tab = feat_table(a.d, a.n);
 
-    auto load = [&](int64_t step) {  // 32 features of the state and of its column d_v; past f1: zeros
+    auto load = [&](int64_t step) {  // 64 features of the state and of z; past f1: zeros
         const int64_t f = f0 + step * kFeats;
         const int buf = (int)(step % kSteps);
         if (f < f1) {
+#pragma unroll
             for (int i = tid; i < kFeats * (kCols / 4); i += 256) {
                 const int r = i / (kCols / 4), c = i % (kCols / 4) * 4;
                 const bool in = f + r < f1 && c < ncol;
                 ptx::cp_async16(&st[buf][r][c], in ? S + (f + r) * a.dv + c0 + c : S, in ? 16 : 0);
             }
-            if (tid < kFeats / 4) {
-                const int64_t left = f1 - f - tid * 4;
-                const bool in = left > 0;
-                ptx::cp_async16(&zt[buf][tid * 4], in ? S + a.F * a.dv + f + tid * 4 : S,
-                                in ? (uint32_t)min64(left, 4) * 4 : 0);
+            if (tid < kFeats) {
+                const bool in = f + tid < f1;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_u32(&st[buf][tid][kCols])),
+                             "l"(in ? S + a.F * a.dv + f + tid : S), "r"(in ? 4 : 0)
+                             : "memory");
             }
         }
         ptx::cp_async_commit();
     };
     for (int i = 0; i < kSteps - 1; ++i) load(i);
+    for (int i = tid; i < kSteps * kFeats * (kPitch - kCols - 1); i += 256) {
+        const int r = i / (kPitch - kCols - 1), c = kCols + 1 + i % (kPitch - kCols - 1);
+        dyn[r * kPitch + c] = 0.f;
+    }
     if (tid < a.n) coef[tid] = query_coeff(tid, a.tau);
     if (a.d * sizeof(T) % 16 == 0) {
         constexpr int E = 16 / sizeof(T);
@@ -138,69 +158,72 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
             packed |= (p < fd.m ? (fd.packed >> (8 * p)) & 0xffu : (uint32_t)a.d) << (8 * p);
         desc[tid] = make_uint2(packed, __float_as_uint(fd.w));
     };
-    const int mq = tid % MB, fg = tid / MB;      // forming features
-    const int mg = tid / 16, cg = tid % 16 * 4;  // multiplying
-    f32x2 acc[TM][2] = {};
-    float z = 0.f;
+    const int g = lane >> 2, t = lane & 3;  // the instruction's row group and column
+    const int mt = warp % MT, ks = warp / MT, m0 = mt * 16;
+    float acc[NT][4] = {};
     describe(f0 + tid);
     int64_t step = 0;
     for (int64_t f = f0; f < f1; f += kFeats, ++step) {
-        const int buf = (int)(step % kSteps), group = (int)(step & 7) * kFeats;
+        const int buf = (int)(step % kSteps), group = (int)(step & 3) * kFeats;
         ptx::cp_async_wait<kSteps - 2>();
         __syncthreads();  // this step's state and descriptors are there, the last step's are free
         load(step + kSteps - 1);
-        float val[PER];
-        uint2 ds[PER];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            ds[i] = desc[group + fg * PER + i];
-            val[i] = __uint_as_float(ds[i].y);
-        }
+        for (int i = 0; i < SLICES; ++i) {
+            const int k0 = (i * KS + ks) * 8;
+            float v[4];  // queries g, g + 8 by features t, t + 4
+            const uint2 d0 = desc[group + k0 + t], d1 = desc[group + k0 + t + 4];
+            v[0] = v[1] = __uint_as_float(d0.y);
+            v[2] = v[3] = __uint_as_float(d1.y);
 #pragma unroll
-        for (int e = 0; e < NF; ++e)
+            for (int e = 0; e < NF; ++e) {
+                const float* x0 = xs[(d0.x >> (8 * e)) & 0xffu] + m0 + g;
+                const float* x1 = xs[(d1.x >> (8 * e)) & 0xffu] + m0 + g;
+                v[0] *= x0[0];
+                v[1] *= x0[8];
+                v[2] *= x1[0];
+                v[3] *= x1[8];
+            }
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) val[i] *= xs[(ds[i].x >> (8 * e)) & 0xffu][mq];
+            for (int e = 0; e < 4; ++e) split_tf32(v[e], hi[e], lo[e]);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            phi[fg * PER + i][mq] = val[i];
-            z = fmaf(val[i], zt[buf][fg * PER + i], z);
-        }
-        __syncthreads();
-#pragma unroll 8
-        for (int r = 0; r < kFeats; ++r) {
-            const ulonglong2 s = *reinterpret_cast<const ulonglong2*>(&st[buf][r][cg]);
-            float p[TM];
-            if constexpr (TM == 4) *reinterpret_cast<float4*>(p) = *reinterpret_cast<const float4*>(&phi[r][mg * 4]);
-            else if constexpr (TM == 2) *reinterpret_cast<float2*>(p) = *reinterpret_cast<const float2*>(&phi[r][mg * 2]);
-            else p[0] = phi[r][mg];
-#pragma unroll
-            for (int t = 0; t < TM; ++t) {
-                const f32x2 pp = make2(p[t], p[t]);
-                acc[t][0] = fma2(pp, s.x, acc[t][0]);
-                acc[t][1] = fma2(pp, s.y, acc[t][1]);
+            for (int n = 0; n < NT; ++n) {
+                uint32_t bh0, bl0, bh1, bl1;
+                split_tf32(st[buf][k0 + t][n * 8 + g], bh0, bl0);
+                split_tf32(st[buf][k0 + t + 4][n * 8 + g], bh1, bl1);
+                mma_tf32(acc[n], lo, bh0, bh1);
+                mma_tf32(acc[n], hi, bl0, bl1);
+                mma_tf32(acc[n], hi, bh0, bh1);
             }
         }
-        if (group == 7 * kFeats && f + kFeats < f1) describe(f + kFeats + tid);
+        if (group == 3 * kFeats && f + kFeats < f1) {
+            __syncthreads();  // every warp has read the descriptors
+            describe(f + kFeats + tid);
+        }
     }
-    const int pitch = a.dv + 4;
-    float* Y = a.part + ((int64_t)split * a.H + h) * a.B * pitch;
+    // the warps of one query tile join in shared memory, where the state was
+    ptx::cp_async_wait<0>();
+    __syncthreads();
+    float(*part)[MB][kPitch] = reinterpret_cast<float(*)[MB][kPitch]>(dyn);  // [KS]
 #pragma unroll
-    for (int t = 0; t < TM; ++t) {
-        const int m = mg * TM + t;
-        if (m < nq && cg < ncol) {
-            const float2 lo = split2(acc[t][0]), hi = split2(acc[t][1]);
-            *reinterpret_cast<float4*>(Y + (int64_t)(b0 + m) * pitch + c0 + cg) = make_float4(lo.x, lo.y, hi.x, hi.y);
-        }
+    for (int n = 0; n < NT; ++n) {
+        *reinterpret_cast<float2*>(&part[ks][m0 + g][n * 8 + 2 * t]) = make_float2(acc[n][0], acc[n][1]);
+        *reinterpret_cast<float2*>(&part[ks][m0 + g + 8][n * 8 + 2 * t]) = make_float2(acc[n][2], acc[n][3]);
     }
-    if (ct == 0) {
-        __syncthreads();
-        phi[fg][mq] = z;
-        __syncthreads();
-        if (tid < nq) {
-            float v = 0.f;
-            for (int g = 0; g < 256 / MB; ++g) v += phi[g][tid];
-            Y[(int64_t)(b0 + tid) * pitch + a.dv] = v;
+    __syncthreads();
+    const int pitch = a.dv + 4;
+    float* Y = a.part + (((int64_t)split * a.H + h) * a.B + b0) * pitch;
+    for (int i = tid; i < nq * (kCols / 4 + 1); i += 256) {
+        const int m = i / (kCols / 4 + 1), c = i % (kCols / 4 + 1) * 4;
+        float4 v = *reinterpret_cast<const float4*>(&part[0][m][c]);
+#pragma unroll
+        for (int k = 1; k < KS; ++k) {
+            const float4 w = *reinterpret_cast<const float4*>(&part[k][m][c]);
+            v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
         }
+        if (c < ncol) *reinterpret_cast<float4*>(Y + (int64_t)m * pitch + c0 + c) = v;
+        else if (c == kCols && ct == 0) Y[(int64_t)m * pitch + a.dv] = v.x;
     }
 }
 
@@ -212,17 +235,17 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
 // read once, in pieces of up to 16 bytes.  Bound by the cache's bytes.  The
 // sums of the lanes, warps and CTAs and the shared part's shares are joined in
 // an order that depends on the sizes alone.
-constexpr int kUnroll = 2;                // tokens of eight lanes in a step
-constexpr int kOwnTokens = 32 * kUnroll;  // of a CTA and step
+constexpr int kUnroll = 2;  // tokens of eight lanes in a step
 
 // Bytes of a token that one lane keeps in shared memory, and the steps that
-// fit into 64 KB a CTA (two at least).
+// fit into 256 bytes a thread (two at least, four at most).
 template <typename T, int KV, int VV, int J>
 constexpr int kLaneBytes = (KV + J * VV) * (int)sizeof(T);
 template <typename T, int KV, int VV, int J>
-constexpr int kAhead = 65536 / (256 * kUnroll * kLaneBytes<T, KV, VV, J>) < 2   ? 2
-                       : 65536 / (256 * kUnroll * kLaneBytes<T, KV, VV, J>) > 4 ? 4
-                                                                                 : 65536 / (256 * kUnroll * kLaneBytes<T, KV, VV, J>);
+constexpr int ahead() {
+    constexpr int fit = 256 / (kUnroll * kLaneBytes<T, KV, VV, J>);
+    return fit < 2 ? 2 : fit > 4 ? 4 : fit;
+}
 
 template <typename T, int N>
 __device__ __forceinline__ void to_pairs(const Span<T, N>& p, f32x2 (&x)[N / 2]) {
@@ -263,12 +286,12 @@ __device__ __forceinline__ void cluster_barrier() {
 
 // KV: entries of k a lane reads at once (0: one by one, any d_k); VV: columns
 // of v it reads at once, J times.
-template <typename T, int KV, int VV, int J>
-__global__ void __launch_bounds__(256, J* VV <= 16 ? 3 : 1)
+template <typename T, int KV, int VV, int J, int NW>
+__global__ void __launch_bounds__(32 * NW, J* VV <= 16 ? 24 / NW : 1)
 prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster) {
-    constexpr int KE = KV ? KV : kMaxDk / 8;
+    constexpr int KE = KV ? KV : kMaxDk / 8, THREADS = 32 * NW, TOKENS = 4 * NW * kUnroll;
     extern __shared__ __align__(16) unsigned char ring[];
-    __shared__ __align__(16) float red[8][kMaxDv + 4];
+    __shared__ __align__(16) float red[NW][kMaxDv + 4];
     __shared__ float tot[kMaxDv + 1];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, sub = lane & 7, grp = lane >> 3;
     const int rank = blockIdx.x % cluster, bh = blockIdx.x / cluster, b = bh / a.H, h = bh - b * a.H;
@@ -279,7 +302,8 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
     const int L = a.lengths[b];
     if (L < 0 || L >= a.cap) {  // the same in every CTA of the cluster
         ptx::pdl_wait_primary();
-        if (rank == 0 && tid < a.dv) a.out[(int64_t)bh * a.dv + tid] = nanf("");
+        if (rank == 0)
+            for (int c = tid; c < a.dv; c += THREADS) a.out[(int64_t)bh * a.dv + c] = nanf("");
         if (rank == 0 && tid == 0) atomicOr(a.err, kErrLength);
         return;
     }
@@ -304,38 +328,38 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
     f32x2 y[J][VV / 2] = {};
     float z = 0.f;
     // tokens ahead, each lane's share in slots that it alone reads
-    constexpr int A = kAhead<T, KV, VV, J>;
-    Span<T, VV>* vring = reinterpret_cast<Span<T, VV>*>(ring);                                  // [A][kUnroll][J][256]
-    Span<T, KE>* kring = reinterpret_cast<Span<T, KE>*>(vring + A * kUnroll * J * 256);         // [A][kUnroll][256]
-    const int stride = cluster * kOwnTokens, mine = warp * 4 + grp, start = rank * kOwnTokens;
+    constexpr int A = ahead<T, KV, VV, J>();
+    Span<T, VV>* vring = reinterpret_cast<Span<T, VV>*>(ring);                                  // [A][kUnroll][J][THREADS]
+    Span<T, KE>* kring = reinterpret_cast<Span<T, KE>*>(vring + A * kUnroll * J * THREADS);         // [A][kUnroll][THREADS]
+    const int stride = cluster * TOKENS, mine = warp * 4 + grp, start = rank * TOKENS;
     // rows of the next step to fetch
     const T* kp = kc + (int64_t)(start + mine) * a.d + sub * KV;
     const T* vp = vc + (int64_t)(start + mine) * a.dv + sub * VV;
     int jf = start;
     const int64_t kstep = (int64_t)stride * a.d, vstep = (int64_t)stride * a.dv;
-    const int ku = 32 * a.d, vu = 32 * a.dv;
+    const int ku = 4 * NW * a.d, vu = 4 * NW * a.dv;
     const bool wide = J * 8 * VV == a.dv;  // every lane's columns exist
     auto fetch = [&](int slot) {
-        Span<T, KE>* kt = &kring[slot * kUnroll * 256 + tid];
-        Span<T, VV>* vt = &vring[slot * kUnroll * J * 256 + tid];
-        if (jf + kOwnTokens <= L && wide) {  // a whole step of cached tokens
+        Span<T, KE>* kt = &kring[slot * kUnroll * THREADS + tid];
+        Span<T, VV>* vt = &vring[slot * kUnroll * J * THREADS + tid];
+        if (jf + TOKENS <= L && wide) {  // a whole step of cached tokens
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                if constexpr (KV > 0) fetch_async<KV * sizeof(T)>(kt + u * 256, kp + u * ku);
+                if constexpr (KV > 0) fetch_async<KV * sizeof(T)>(kt + u * THREADS, kp + u * ku);
 #pragma unroll
-                for (int i = 0; i < J; ++i) fetch_async<VV * sizeof(T)>(vt + (u * J + i) * 256, vp + u * vu + i * 8 * VV);
+                for (int i = 0; i < J; ++i) fetch_async<VV * sizeof(T)>(vt + (u * J + i) * THREADS, vp + u * vu + i * 8 * VV);
             }
         } else {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int j = jf + u * 32 + mine;
+                const int j = jf + u * 4 * NW + mine;
                 if (j <= L) {  // the new token comes from k and v
-                    if constexpr (KV > 0) fetch_async<KV * sizeof(T)>(kt + u * 256, j < L ? kp + u * ku : k + sub * KV);
+                    if constexpr (KV > 0) fetch_async<KV * sizeof(T)>(kt + u * THREADS, j < L ? kp + u * ku : k + sub * KV);
 #pragma unroll
                     for (int i = 0; i < J; ++i) {
                         const int c = (i * 8 + sub) * VV;
                         if (c < a.dv)
-                            fetch_async<VV * sizeof(T)>(vt + (u * J + i) * 256, j < L ? vp + u * vu + i * 8 * VV : v + c);
+                            fetch_async<VV * sizeof(T)>(vt + (u * J + i) * THREADS, j < L ? vp + u * vu + i * 8 * VV : v + c);
                     }
                 }
             }
@@ -350,11 +374,11 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
         Span<T, VV> vr[kUnroll][J];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int j = j0 + u * 32 + mine;
+            const int j = j0 + u * 4 * NW + mine;
             const bool in = whole || j <= L;
             kr[u] = {};
             if constexpr (KV > 0) {
-                if (in) kr[u] = kring[(slot * kUnroll + u) * 256 + tid];
+                if (in) kr[u] = kring[(slot * kUnroll + u) * THREADS + tid];
             } else {
                 const T* krow = j < L ? kc + (int64_t)j * a.d : k;
 #pragma unroll
@@ -364,7 +388,7 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
 #pragma unroll
             for (int i = 0; i < J; ++i) {
                 vr[u][i] = {};
-                if (whole || (in && (i * 8 + sub) * VV < a.dv)) vr[u][i] = vring[((slot * kUnroll + u) * J + i) * 256 + tid];
+                if (whole || (in && (i * 8 + sub) * VV < a.dv)) vr[u][i] = vring[((slot * kUnroll + u) * J + i) * THREADS + tid];
             }
         }
         float x[kUnroll];
@@ -385,7 +409,7 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             float w = fmaf(x[u], fmaf(x[u], fmaf(x[u], fmaf(x[u], c4, c3), c2), c1), 1.f);
-            if (!whole && j0 + u * 32 + mine > L) w = 0.f;
+            if (!whole && j0 + u * 4 * NW + mine > L) w = 0.f;
             z += w;
             const f32x2 ww = make2(w, w);
 #pragma unroll
@@ -404,7 +428,7 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
     for (int j0 = start; j0 <= L; j0 += stride) {
         fetch(slot == 0 ? A - 1 : slot - 1);
         ptx::cp_async_wait<A - 1>();
-        if (j0 + kOwnTokens <= L && wide) consume(std::true_type{}, j0, slot);
+        if (j0 + TOKENS <= L && wide) consume(std::true_type{}, j0, slot);
         else consume(std::false_type{}, j0, slot);
         if (++slot == A) slot = 0;
     }
@@ -438,7 +462,7 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
         const int pitch = a.dv + 4;
         for (int c = lane * 4; c <= a.dv; c += 128) {
             float4 s = *reinterpret_cast<float4*>(&red[warp][c]);
-            for (int i = warp; i < splits; i += 8) {
+            for (int i = warp; i < splits; i += NW) {
                 const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part + (((int64_t)i * a.H + h) * a.B + b) * pitch + c));
                 s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
             }
@@ -446,16 +470,16 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
         }
     }
     __syncthreads();
-    for (int c = tid; c <= a.dv; c += 256) {
+    for (int c = tid; c <= a.dv; c += THREADS) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) s += red[w][c];
+        for (int w = 0; w < NW; ++w) s += red[w][c];
         tot[c] = s;
     }
     if (cluster > 1) {
         cluster_barrier();
         if (rank == 0)
-            for (int c = tid; c <= a.dv; c += 256) {
+            for (int c = tid; c <= a.dv; c += THREADS) {
                 float s = tot[c];
                 for (int i = 1; i < cluster; ++i) s += load_remote(&tot[c], i);
                 tot[c] = s;
@@ -464,9 +488,9 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
     }
     __syncthreads();
     if (rank == 0) {
-        if (tid < a.dv) {
-            a.out[(int64_t)bh * a.dv + tid] = tot[tid] / tot[a.dv];
-            vc[(int64_t)L * a.dv + tid] = v[tid];
+        for (int c = tid; c < a.dv; c += THREADS) {
+            a.out[(int64_t)bh * a.dv + c] = tot[c] / tot[a.dv];
+            vc[(int64_t)L * a.dv + c] = v[c];
         }
         if (tid < a.d) kc[(int64_t)L * a.d + tid] = k[tid];
     }
@@ -476,32 +500,32 @@ struct OwnKernel {
     void (*run)(PrefixArgs, int, int);
     int smem;
 };
-template <typename T, int KV, int VV, int J>
+template <typename T, int KV, int VV, int J, int NW>
 OwnKernel own_of() {
-    return {prefix_own_kernel<T, KV, VV, J>, 256 * kUnroll * kAhead<T, KV, VV, J> * kLaneBytes<T, KV, VV, J>};
+    return {prefix_own_kernel<T, KV, VV, J, NW>, 32 * NW * kUnroll * ahead<T, KV, VV, J>() * kLaneBytes<T, KV, VV, J>};
 }
-template <typename T, int KV, int VV>
+template <typename T, int KV, int NW, int VV>
 OwnKernel own_kernel_j(int dv) {
     const int j = (dv + 8 * VV - 1) / (8 * VV);
-    if (j <= 1) return own_of<T, KV, VV, 1>();
-    if (j <= 2) return own_of<T, KV, VV, 2>();
+    if (j <= 1) return own_of<T, KV, VV, 1, NW>();
+    if (j <= 2) return own_of<T, KV, VV, 2, NW>();
     if constexpr (VV == 4)
-        if (j > 4) return own_of<T, KV, 4, 8>();
-    return own_of<T, KV, VV, 4>();
+        if (j > 4) return own_of<T, KV, 4, 8, NW>();
+    return own_of<T, KV, VV, 4, NW>();
 }
-template <typename T, int KV>
+template <typename T, int KV, int NW>
 OwnKernel own_kernel_v(int dv) {
     // 16-byte pieces of v where its rows hold whole ones for all lanes
     if constexpr (sizeof(T) == 2)
-        if (dv % 64 == 0) return own_kernel_j<T, KV, 8>(dv);
-    return own_kernel_j<T, KV, 4>(dv);
+        if (dv % 64 == 0) return own_kernel_j<T, KV, NW, 8>(dv);
+    return own_kernel_j<T, KV, NW, 4>(dv);
 }
-template <typename T>
+template <typename T, int NW>
 OwnKernel own_kernel(int d, int dv) {
-    if (d == 64) return own_kernel_v<T, 8>(dv);
-    if (d == 32) return own_kernel_v<T, 4>(dv);
-    if (d == 16) return own_kernel_v<T, 2>(dv);
-    return own_kernel_v<T, 0>(dv);
+    if (d == 64) return own_kernel_v<T, 8, NW>(dv);
+    if (d == 32) return own_kernel_v<T, 4, NW>(dv);
+    if (d == 16) return own_kernel_v<T, 2, NW>(dv);
+    return own_kernel_v<T, 0, NW>(dv);
 }
 
 template <typename T, int MB>
@@ -522,30 +546,32 @@ auto state_kernel(int MB, int n) {
 template <typename T>
 cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
     const int sms = entry::num_sms();
-    // the shared part: two CTAs an SM, a share of at least 32 features each
+    // the shared part: two CTAs an SM, a share of at least 64 features each
     const int MB = a.B <= 16 ? 16 : a.B <= 32 ? 32 : 64;
     const int btiles = (a.B + MB - 1) / MB, ctiles = (a.dv + kCols - 1) / kCols;
     const int64_t tiles = (int64_t)a.H * btiles * ctiles, all = (a.F + kFeats - 1) / kFeats;
-    int64_t splits = PREFIX_FILL * sms / tiles;
+    int64_t splits = 2 * sms / tiles;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits > all) splits = all;
     if (splits < 1) splits = 1;
     const int64_t steps = (all + splits - 1) / splits;
     splits = (all + steps - 1) / steps;
-    // the own tokens: CTAs of one sequence and head share them while that
-    // leaves each a few steps and the GPU has room
+    // the own tokens: four warps a sequence and head where those CTAs fill the
+    // GPU (more of them stay in flight while some begin and others end), else
+    // eight, and while that leaves each 256 tokens a cluster of CTAs
     const int64_t heads = (int64_t)a.B * a.H;
-    int64_t cluster = (int64_t)sms * 4 / heads, room = ((int64_t)a.cap + 4 * kOwnTokens - 1) / (4 * kOwnTokens);
+    const bool many = heads >= 2 * (int64_t)sms;
+    int64_t cluster = (int64_t)sms * 4 / heads, room = ((int64_t)a.cap + 255) / 256;
     if (cluster > room) cluster = room;
     if (cluster > 8) cluster = 8;
-    if (cluster < 1) cluster = 1;
+    if (cluster < 1 || many) cluster = 1;
 
     const size_t bytes = (size_t)splits * heads * (a.dv + 4) * sizeof(float);
     cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&a.part), bytes, stream);
     if (e != cudaSuccess) return e;
     const auto state = state_kernel<T>(MB, a.n);
-    const size_t smem = (size_t)(kSteps * kFeats * (kCols + 1) + (a.d + 1) * MB) * sizeof(float);
-    const OwnKernel own = own_kernel<T>(a.d, a.dv);
+    const size_t smem = (size_t)(kSteps * kFeats * kPitch + (a.d + 1) * (MB + 8)) * sizeof(float);
+    const OwnKernel own = many ? own_kernel<T, 4>(a.d, a.dv) : own_kernel<T, 8>(a.d, a.dv);
     if ((e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(own.run, cudaFuncAttributeMaxDynamicSharedMemorySize, own.smem)) != cudaSuccess) {
         workspace_free(a.part, stream);
@@ -557,7 +583,7 @@ cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(heads * cluster));
-        cfg.blockDim = dim3(256);
+        cfg.blockDim = dim3(many ? 128 : 256);
         cfg.dynamicSmemBytes = own.smem;
         cfg.stream = stream;
         cudaLaunchAttribute attr[2];
