@@ -12,6 +12,7 @@
 // that it keeps its digits where a is near 1.
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -526,7 +527,8 @@ cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
     if (!err) return cudaErrorUnknown;
     auto kernel = scan_kernel<T, V, BWD>;
     if (smem > 0) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = entry::allow_smem(kernel, (int)smem, done);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

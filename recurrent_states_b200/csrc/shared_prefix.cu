@@ -12,6 +12,7 @@
 // its own.  The new k and v are appended to the cache in the same call.
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -231,10 +232,15 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
 // One cluster of CTAs per sequence and head (one CTA but for long suffixes of
 // few heads).  Eight lanes take a token: each multiplies its share of q and k,
 // three shuffles make the score, and with the weight K(tau q.k) each adds its
-// share of v, so a warp has four tokens a step and U steps in flight; rows are
-// read once, in pieces of up to 16 bytes.  Bound by the cache's bytes.  The
-// sums of the lanes, warps and CTAs and the shared part's shares are joined in
-// an order that depends on the sizes alone.
+// share of v.  Rows are read once, in pieces of up to 16 bytes, by asynchronous
+// copies into slots that one lane alone reads, several steps ahead.  The sums
+// of the lanes, warps and CTAs and the shared part's shares are joined in an
+// order that depends on the sizes alone.
+//
+// The cache's bytes bound it: 64 sequences of 16 heads, d 64 and 64, up to
+// 1,024 own tokens (144 MB) take 45 us with the shared part beside them, 3.2
+// TB/s; tokens in registers 68 us, with selects on every token 55 us.  What is
+// left is the start and end of each CTA (2 to 4 us of some 15).
 constexpr int kUnroll = 2;  // tokens of eight lanes in a step
 
 // Bytes of a token that one lane keeps in shared memory, and the steps that
@@ -423,6 +429,10 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
     };
 #pragma unroll 1
     for (int i = 0; i < A - 1; ++i) fetch(i);
+    if (rank == 0) {  // append the new token, whose row of the cache nobody reads here
+        for (int c = tid; c < a.dv; c += THREADS) vc[(int64_t)L * a.dv + c] = v[c];
+        if (tid < a.d) kc[(int64_t)L * a.d + tid] = k[tid];
+    }
     int slot = 0;
 #pragma unroll 1
     for (int j0 = start; j0 <= L; j0 += stride) {
@@ -460,11 +470,19 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
     if (rank == 0) {  // the shared part's shares, warp by warp
         ptx::pdl_wait_primary();
         const int pitch = a.dv + 4;
+        const int64_t heads = (int64_t)a.B * a.H;
         for (int c = lane * 4; c <= a.dv; c += 128) {
             float4 s = *reinterpret_cast<float4*>(&red[warp][c]);
-            for (int i = warp; i < splits; i += NW) {
-                const float4 p = __ldcg(reinterpret_cast<const float4*>(a.part + (((int64_t)i * a.H + h) * a.B + b) * pitch + c));
-                s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+            const float* from = a.part + ((int64_t)h * a.B + b) * pitch + c;
+            const int64_t share = heads * pitch;
+            for (int i0 = warp; i0 < splits; i0 += 4 * NW) {  // four loads in flight
+                float4 p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    p[i] = i0 + i * NW < splits ? __ldcg(reinterpret_cast<const float4*>(from + (i0 + i * NW) * share))
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s.x += p[i].x, s.y += p[i].y, s.z += p[i].z, s.w += p[i].w;
             }
             *reinterpret_cast<float4*>(&red[warp][c]) = s;
         }
@@ -488,21 +506,20 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
     }
     __syncthreads();
     if (rank == 0) {
-        for (int c = tid; c < a.dv; c += THREADS) {
-            a.out[(int64_t)bh * a.dv + c] = tot[c] / tot[a.dv];
-            vc[(int64_t)L * a.dv + c] = v[c];
-        }
-        if (tid < a.d) kc[(int64_t)L * a.d + tid] = k[tid];
+        for (int c = tid; c < a.dv; c += THREADS) a.out[(int64_t)bh * a.dv + c] = tot[c] / tot[a.dv];
     }
 }
 
 struct OwnKernel {
     void (*run)(PrefixArgs, int, int);
     int smem;
+    std::atomic<uint64_t>* done;
 };
 template <typename T, int KV, int VV, int J, int NW>
 OwnKernel own_of() {
-    return {prefix_own_kernel<T, KV, VV, J, NW>, 32 * NW * kUnroll * ahead<T, KV, VV, J>() * kLaneBytes<T, KV, VV, J>};
+    static std::atomic<uint64_t> done{0};
+    return {prefix_own_kernel<T, KV, VV, J, NW>, 32 * NW * kUnroll * ahead<T, KV, VV, J>() * kLaneBytes<T, KV, VV, J>,
+            &done};
 }
 template <typename T, int KV, int NW, int VV>
 OwnKernel own_kernel_j(int dv) {
@@ -528,39 +545,53 @@ OwnKernel own_kernel(int d, int dv) {
     return own_kernel_v<T, 0, NW>(dv);
 }
 
+struct StateKernel {
+    void (*run)(PrefixArgs, int, int, int, int);
+    std::atomic<uint64_t>* done;
+};
+template <typename T, int MB, int NF>
+StateKernel state_of() {
+    static std::atomic<uint64_t> done{0};
+    return {prefix_state_kernel<T, MB, NF>, &done};
+}
 template <typename T, int MB>
-auto state_kernel_n(int n) {
+StateKernel state_kernel_n(int n) {
     switch (n) {
-        case 1: return prefix_state_kernel<T, MB, 0>;
-        case 2: return prefix_state_kernel<T, MB, 1>;
-        case 3: return prefix_state_kernel<T, MB, 2>;
-        case 4: return prefix_state_kernel<T, MB, 3>;
-        default: return prefix_state_kernel<T, MB, 4>;
+        case 1: return state_of<T, MB, 0>();
+        case 2: return state_of<T, MB, 1>();
+        case 3: return state_of<T, MB, 2>();
+        case 4: return state_of<T, MB, 3>();
+        default: return state_of<T, MB, 4>();
     }
 }
 template <typename T>
-auto state_kernel(int MB, int n) {
+StateKernel state_kernel(int MB, int n) {
     return MB == 16 ? state_kernel_n<T, 16>(n) : MB == 32 ? state_kernel_n<T, 32>(n) : state_kernel_n<T, 64>(n);
 }
+constexpr int state_smem(int MB, int d) { return (kSteps * kFeats * kPitch + (d + 1) * (MB + 8)) * (int)sizeof(float); }
 
 template <typename T>
 cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
     const int sms = entry::num_sms();
-    // the shared part: two CTAs an SM, a share of at least 64 features each
+    // the shared part: a CTA an SM, a share of at least 64 features each (twice
+    // as many gain nothing: their sums have to be joined)
     const int MB = a.B <= 16 ? 16 : a.B <= 32 ? 32 : 64;
     const int btiles = (a.B + MB - 1) / MB, ctiles = (a.dv + kCols - 1) / kCols;
     const int64_t tiles = (int64_t)a.H * btiles * ctiles, all = (a.F + kFeats - 1) / kFeats;
-    int64_t splits = 2 * sms / tiles;
+    int64_t splits = sms / tiles;
     if (splits > kMaxSplits) splits = kMaxSplits;
     if (splits > all) splits = all;
     if (splits < 1) splits = 1;
     const int64_t steps = (all + splits - 1) / splits;
     splits = (all + steps - 1) / steps;
-    // the own tokens: four warps a sequence and head where those CTAs fill the
-    // GPU (more of them stay in flight while some begin and others end), else
-    // eight, and while that leaves each 256 tokens a cluster of CTAs
+    // the own tokens: four warps a sequence and head where there are many and
+    // none is long (more CTAs stay in flight while some begin and others end:
+    // 1,024 heads of up to 512 tokens, d 16, 19.8 us, at eight warps 22.4; 4,096
+    // of up to 512, d 64, 91 and 99 us), else eight (a long one would still run
+    // when the others are done: 1,024 of up to 1,024, d 64, 48 and 45 us), and
+    // while that leaves each 256 tokens a cluster of CTAs
     const int64_t heads = (int64_t)a.B * a.H;
-    const bool many = heads >= 2 * (int64_t)sms;
+    const bool many = heads >= 2 * (int64_t)sms && (int64_t)a.cap * (a.d + a.dv) * (int64_t)sizeof(T) <= 192 * 1024;
     int64_t cluster = (int64_t)sms * 4 / heads, room = ((int64_t)a.cap + 255) / 256;
     if (cluster > room) cluster = room;
     if (cluster > 8) cluster = 8;
@@ -569,16 +600,16 @@ cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
     const size_t bytes = (size_t)splits * heads * (a.dv + 4) * sizeof(float);
     cudaError_t e = workspace_alloc(reinterpret_cast<void**>(&a.part), bytes, stream);
     if (e != cudaSuccess) return e;
-    const auto state = state_kernel<T>(MB, a.n);
-    const size_t smem = (size_t)(kSteps * kFeats * kPitch + (a.d + 1) * (MB + 8)) * sizeof(float);
+    const StateKernel state = state_kernel<T>(MB, a.n);
     const OwnKernel own = many ? own_kernel<T, 4>(a.d, a.dv) : own_kernel<T, 8>(a.d, a.dv);
-    if ((e = cudaFuncSetAttribute(state, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(own.run, cudaFuncAttributeMaxDynamicSharedMemorySize, own.smem)) != cudaSuccess) {
+    if ((e = entry::allow_smem(state.run, state_smem(MB, kMaxDk), *state.done)) != cudaSuccess ||
+        (e = entry::allow_smem(own.run, own.smem, *own.done)) != cudaSuccess) {
         workspace_free(a.part, stream);
         return e;
     }
     TA_TIMED(stream, "prefix_state_kernel",
-             state<<<(unsigned)(tiles * splits), 256, smem, stream>>>(a, (int)splits, ctiles, btiles, (int)steps));
+             state.run<<<(unsigned)(tiles * splits), 256, state_smem(MB, a.d), stream>>>(a, (int)splits, ctiles, btiles,
+                                                                                         (int)steps));
     e = cudaGetLastError();
     if (e == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
