@@ -121,7 +121,10 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 // its reads of round i.
 constexpr int kTile = 32;     // channels of a CTA
 constexpr int kStages = 2;
-constexpr int kMaxCluster = 8;
+#ifndef SCAN_MC
+#define SCAN_MC 8
+#endif
+constexpr int kMaxCluster = SCAN_MC;
 constexpr uint32_t kWait = 1u << 24;  // polls of a cluster's totals
 
 template <typename T, int V>
@@ -240,21 +243,21 @@ constexpr int elements() {
     return 32 / (int)sizeof(T) / (BWD ? 2 : 1) * (kSingles<T, V, BWD> ? 1 : 2);
 }
 template <typename T, int V, bool BWD>
-constexpr int kCtas = kSingles<T, V, BWD> ? 3 : 2;  // CTAs an SM holds
+constexpr int kSmWarps = kSingles<T, V, BWD> ? 24 : 16;  // warps an SM holds
 
-template <typename T, int V, bool BWD>
-__global__ void __launch_bounds__(256, kCtas<T, V, BWD>)
+template <typename T, int V, bool BWD, int W>
+__global__ void __launch_bounds__(32 * W, kSmWarps<T, V, BWD> / W)
 scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int rounds, unsigned int* err) {
     constexpr int LC = kTile / V, GROUPS = 32 / LC;   // lanes of a token; token groups of a warp
     constexpr int R = elements<T, V, BWD>() / V;         // tokens of a thread
-    constexpr int CT = 8 * GROUPS * R;                // tokens of a chunk
+    constexpr int CT = W * GROUPS * R;                // tokens of a chunk
     constexpr int K = BWD ? 4 : 2;                    // gate, x, h before, dh
-    constexpr int P = kPairs<V>;
+    constexpr int P = kPairs<V>, kThreads = 32 * W;
     constexpr bool kAsync = V * sizeof(T) >= 4;
     using Piece = Chans<T, V>;
     extern __shared__ __align__(16) unsigned char raw[];
     Piece* slots = reinterpret_cast<Piece*>(raw);     // [stage][array][token][thread]
-    __shared__ float2 warps[2][8][kTile];             // a warp's (A, b), per parity of the round
+    __shared__ float2 warps[2][W][kTile];             // a warp's (A, b), per parity of the round
     __shared__ float2 ctas[2][kMaxCluster][kTile];    // a CTA's, sent by it to every CTA
     __shared__ __align__(8) uint64_t bars[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -308,7 +311,7 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
     auto fetch = [&](int round) {
         if constexpr (kAsync) {
             if (round < rounds) {
-                Piece* to = slots + (round % kStages) * K * R * 256 + tid;
+                Piece* to = slots + (round % kStages) * K * R * kThreads + tid;
                 const int t0 = token(round);
                 const bool all = whole(round);
 #pragma unroll
@@ -316,11 +319,11 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
                     const T* p = src[k] + t0 * step[k];
                     if (all) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r, p += DIR * step[k]) fetch_async<sizeof(Piece)>(to + (k * R + r) * 256, p);
+                        for (int r = 0; r < R; ++r, p += DIR * step[k]) fetch_async<sizeof(Piece)>(to + (k * R + r) * kThreads, p);
                     } else {
 #pragma unroll
                         for (int r = 0; r < R; ++r, p += DIR * step[k])
-                            if (used(t0 + DIR * r, k)) fetch_async<sizeof(Piece)>(to + (k * R + r) * 256, p);
+                            if (used(t0 + DIR * r, k)) fetch_async<sizeof(Piece)>(to + (k * R + r) * kThreads, p);
                     }
                 }
             }
@@ -335,9 +338,9 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         fetch(round + kStages - 1);
         ptx::cp_async_wait<kStages - 1>();
         const int t0 = token(round);
-        const Piece* mine = slots + (round % kStages) * K * R * 256 + tid;
+        const Piece* mine = slots + (round % kStages) * K * R * kThreads + tid;
         auto piece = [&](int k, int r) {
-            if constexpr (kAsync) return mine[(k * R + r) * 256];
+            if constexpr (kAsync) return mine[(k * R + r) * kThreads];
             else return *reinterpret_cast<const Piece*>(src[k] + (t0 + DIR * r) * step[k]);
         };
         const bool all = whole(round);
@@ -401,15 +404,15 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
             if (warp == 0) {
                 float2 total = warps[par][0][lane];
 #pragma unroll
-                for (int w = 1; w < 8; ++w) {
+                for (int w = 1; w < W; ++w) {
                     const float2 p = warps[par][w][lane];
                     total = make_float2(total.x * p.x, fmaf(p.x, total.y, p.y));
                 }
                 for (int i = 0; i < cluster; ++i) send(&ctas[par][rank][lane], &bars[par], i, total);
             }
-            float2 before[7];
+            float2 before[W - 1];
 #pragma unroll
-            for (int w = 0; w < 7; ++w) before[w] = w < warp ? warps[par][w][lane] : make_float2(1.f, 0.f);
+            for (int w = 0; w < W - 1; ++w) before[w] = w < warp ? warps[par][w][lane] : make_float2(1.f, 0.f);
             if (!lost && !ptx::mbar_wait(&bars[par], (round >> 1) & 1, kWait)) {
                 // never in a sound run: the outputs from here on are not to be used
                 lost = true;
@@ -421,10 +424,10 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
                 run = fmaf(p.x, run, p.y);
             }
 #pragma unroll
-            for (int w = 0; w < 7; ++w) c = fmaf(before[w].x, c, before[w].y);
+            for (int w = 0; w < W - 1; ++w) c = fmaf(before[w].x, c, before[w].y);
         } else {
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < W; ++w) {
                 if (w == warp) c = run;
                 const float2 p = warps[par][w][lane];
                 run = fmaf(p.x, run, p.y);
@@ -509,15 +512,15 @@ bool in_pieces(const ScanArgs& a, int V) {
     return true;
 }
 
-template <typename T, int V, bool BWD>
-cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
-    constexpr int CT = 8 * elements<T, V, BWD>();  // 8 warps x 32 lanes x elements / 32 channels
-    constexpr size_t smem = V * sizeof(T) >= 4 ? (size_t)kStages * (BWD ? 4 : 2) * elements<T, V, BWD>() * sizeof(T) * 256 : 0;
+template <typename T, int V, bool BWD, int W>
+cudaError_t launch_scan_w(const ScanArgs& a, cudaStream_t stream) {
+    constexpr int CT = W * elements<T, V, BWD>();  // warps x 32 lanes x elements / 32 channels
+    constexpr size_t smem = V * sizeof(T) >= 4 ? (size_t)kStages * (BWD ? 4 : 2) * elements<T, V, BWD>() * sizeof(T) * 32 * W : 0;
     const int64_t tiles = (a.D + kTile - 1) / kTile, work = tiles * a.B;
     const int64_t chunks = (a.N + CT - 1) / CT;
     // CTAs that fit at once share a sequence while there are more of them than
     // channel tiles
-    int64_t cluster = (int64_t)entry::num_sms() * kCtas<T, V, BWD> / work;
+    int64_t cluster = (int64_t)entry::num_sms() * (kSmWarps<T, V, BWD> / W) / work;
     if (cluster > chunks) cluster = chunks;
     if (cluster > kMaxCluster) cluster = kMaxCluster;
     if (cluster < 1) cluster = 1;
@@ -525,15 +528,16 @@ cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
     const int rounds = (int)((chunks + cluster - 1) / cluster);
     unsigned int* err = device_error_word();
     if (!err) return cudaErrorUnknown;
-    auto kernel = scan_kernel<T, V, BWD>;
+    auto kernel = scan_kernel<T, V, BWD, W>;
     if (smem > 0) {
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = entry::allow_smem(kernel, (int)smem, done);
         if (e != cudaSuccess) return e;
+        if (SCAN_MC > 8) cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(work * cluster));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(32 * W);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -546,6 +550,19 @@ cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
     TA_TIMED(stream, BWD ? "scan_kernel_backward" : "scan_kernel_forward",
              e = cudaLaunchKernelEx(&cfg, kernel, a, (int)tiles, (int)cluster, rounds, err));
     return e;
+}
+
+// Four warps a CTA where its channel tiles, or the chunks of a short sequence,
+// make enough of them: four CTAs an SM wait for one another's joins less than
+// two of eight (B4 N8192 D1024 bf16: 51 and 92 us, with eight 54 and 99).
+// Eight where a cluster's size limits how many warps share a tile (B1 N65536
+// D512: 98 and 180 us, with four 113 and 195).
+template <typename T, int V, bool BWD>
+cudaError_t launch_scan_v(const ScanArgs& a, cudaStream_t stream) {
+    constexpr int CT = 4 * elements<T, V, BWD>();
+    const int64_t work = (int64_t)((a.D + kTile - 1) / kTile) * a.B;
+    const bool four = a.N <= kMaxCluster * CT || work * kMaxCluster >= 4 * (int64_t)entry::num_sms();
+    return four ? launch_scan_w<T, V, BWD, 4>(a, stream) : launch_scan_w<T, V, BWD, 8>(a, stream);
 }
 
 template <typename T, bool BWD>
