@@ -9,7 +9,9 @@ C names; shape arguments (B, H, N, d_k, d_v) are read from the tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 from typing import Optional, Tuple
 
 import numpy as np
@@ -410,8 +412,10 @@ def taylor_attn_state_merge(a, b, d_k: int, d_v: int, n: int, out=None, stream=N
     return out
 
 
-_Three = _I64 * 3
-_Two = _I64 * 2
+# Host arrays of the calls (strides, frequencies) go as bytes, which ctypes
+# passes by address; building a ctypes array takes five times as long.
+_three = struct.Struct("3q").pack
+_two = struct.Struct("2q").pack
 
 
 def _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype):
@@ -428,10 +432,10 @@ def _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype):
         _want(k_weight, "k_weight", torch.float32, dev, (d,))
     if positions is not None:
         _want(positions, "positions", torch.int64, dev, (B, N))
-    freqs = np.ascontiguousarray(freqs, dtype=np.float64)
+    freqs = np.asarray(freqs, dtype=np.float64)
     if freqs.ndim != 1:
         raise ValueError("freqs must hold one frequency for each rotated pair")
-    return B, N, Hq, Hk, d, dev, qs, ks, freqs
+    return B, N, Hq, Hk, d, dev, qs, ks, 2 * len(freqs), freqs.tobytes()
 
 
 def _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight, interleaved, eps, q_out, k_out,
@@ -440,7 +444,7 @@ def _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight,
         with _on(q, stream):
             return _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight, interleaved, eps,
                                  q_out, k_out, None)
-    B, N, Hq, Hk, d, dev, qs, ks, freqs = _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype)
+    B, N, Hq, Hk, d, dev, qs, ks, rot, table = _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype)
     if q_out is None:
         q_out = q.new_empty(B, Hq, N, d)
     else:
@@ -450,8 +454,8 @@ def _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight,
     else:
         _want(k_out, "k_out", dtype, dev, (B, Hk, N, d))
     rc = getattr(lib(), name)(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), _ptr(positions), pos0,
-                              freqs.ctypes.data, 2 * len(freqs), bool(interleaved), q_out.data_ptr(),
-                              k_out.data_ptr(), B, N, Hq, Hk, d, _Three(*qs[:3]), _Three(*ks[:3]), eps,
+                              table, rot, bool(interleaved), q_out.data_ptr(),
+                              k_out.data_ptr(), B, N, Hq, Hk, d, _three(*qs[:3]), _three(*ks[:3]), eps,
                               _current(dev))
     if rc:
         raise TaylorAttnError(rc, name)
@@ -481,7 +485,7 @@ def _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, 
         with _on(q, stream):
             return _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, pos0, q_weight,
                                           k_weight, interleaved, eps, dq, dk, None)
-    B, N, Hq, Hk, d, dev, qs, ks, freqs = _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype)
+    B, N, Hq, Hk, d, dev, qs, ks, rot, table = _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype)
     _want(dq_out, "dq_out", dtype, dev, (B, Hq, N, d))
     _want(dk_out, "dk_out", dtype, dev, (B, Hk, N, d))
     if dq is None:
@@ -493,9 +497,9 @@ def _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, 
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     rc = getattr(lib(), name)(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), _ptr(q_weight),
-                              _ptr(k_weight), _ptr(positions), pos0, freqs.ctypes.data, 2 * len(freqs),
+                              _ptr(k_weight), _ptr(positions), pos0, table, rot,
                               bool(interleaved), dq.data_ptr(), dk.data_ptr(), _ptr(dqw), _ptr(dkw), B, N, Hq, Hk, d,
-                              _Three(*qs[:3]), _Three(*ks[:3]), _Three(*dqs[:3]), _Three(*dks[:3]), eps,
+                              _three(*qs[:3]), _three(*ks[:3]), _three(*dqs[:3]), _three(*dks[:3]), eps,
                               _current(dev))
     if rc:
         raise TaylorAttnError(rc, name)
@@ -549,7 +553,7 @@ def _gated_scan(name, dtype, gate, x, coupled, h0, lengths, h, h_last, stream):
     elif h_last is not None:
         _want(h_last, "h_last", torch.float32, dev, (B, D))
     rc = getattr(lib(), name)(gate.data_ptr(), x.data_ptr(), _ptr(h0), _ptr(lengths), h.data_ptr(), _ptr(h_last), B, N,
-                              D, _Two(*gs[:2]), _Two(*xs[:2]), bool(coupled), _current(dev))
+                              D, _two(*gs[:2]), _two(*xs[:2]), bool(coupled), _current(dev))
     if rc:
         raise TaylorAttnError(rc, name)
     return h, h_last
@@ -593,8 +597,8 @@ def _gated_scan_backward(name, dtype, gate, x, h, dh, coupled, h0, lengths, dh_l
     elif dh0 is not None:
         _want(dh0, "dh0", torch.float32, dev, (B, D))
     rc = getattr(lib(), name)(gate.data_ptr(), x.data_ptr(), h.data_ptr(), dh.data_ptr(), _ptr(h0), _ptr(lengths),
-                              _ptr(dh_last), dgate.data_ptr(), dx.data_ptr(), _ptr(dh0), B, N, D, _Two(*gs[:2]),
-                              _Two(*xs[:2]), _Two(*dgs[:2]), _Two(*dxs[:2]), bool(coupled), _current(dev))
+                              _ptr(dh_last), dgate.data_ptr(), dx.data_ptr(), _ptr(dh0), B, N, D, _two(*gs[:2]),
+                              _two(*xs[:2]), _two(*dgs[:2]), _two(*dxs[:2]), bool(coupled), _current(dev))
     if rc:
         raise TaylorAttnError(rc, name)
     return dgate, dx, dh0
@@ -655,6 +659,11 @@ def taylor_attn_gated_step_f32(gate, x, state, coupled: bool = True, out=None, s
     return _gated_step("taylor_attn_gated_step_f32", torch.float32, gate, x, state, coupled, out, state_out, stream)
 
 
+@functools.lru_cache(maxsize=256)
+def _stride_of(d_k: int, d_v: int, n: int) -> int:
+    return taylor_attn_state_stride(d_k, d_v, n)
+
+
 def _shared_prefix_decode(name, dtype, q, k, v, prefix_state, k_cache, v_cache, lengths, n, tau, out, stream):
     if _elsewhere(q, stream):
         with _on(q, stream):
@@ -664,7 +673,7 @@ def _shared_prefix_decode(name, dtype, q, k, v, prefix_state, k_cache, v_cache, 
         raise ValueError("q, k must be [B, H, d_k], v [B, H, d_v] and the caches [B, H, cap, d]")
     B, H, d_k = q.shape
     d_v, cap, dev = v.size(-1), k_cache.size(2), q.get_device()
-    stride = lib().taylor_attn_state_stride(d_k, d_v, n)
+    stride = _stride_of(d_k, d_v, n)
     if stride < 0:
         raise TaylorAttnError(TAYLOR_ERR_UNSUPPORTED, name)
     _want(q, "q", dtype, dev, q.shape)
@@ -675,7 +684,7 @@ def _shared_prefix_decode(name, dtype, q, k, v, prefix_state, k_cache, v_cache, 
     _want(v_cache, "v_cache", dtype, dev, (B, H, cap, d_v))
     _want(lengths, "lengths", torch.int32, dev, (B,))
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=torch.float32, device=q.device)
+        out = prefix_state.new_empty(B, H, d_v)
     else:
         _want(out, "out", torch.float32, dev, (B, H, d_v))
     rc = getattr(lib(), name)(q.data_ptr(), k.data_ptr(), v.data_ptr(), prefix_state.data_ptr(), k_cache.data_ptr(),
