@@ -111,9 +111,10 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 // Memory bounds the operator, 6 B a value forward and 12 B backward in bf16;
 // this kernel is bound by instructions and the latency of its rounds: 25 and
 // 49 instructions a value, issue slots 54 % taken at 14 warps an SM.  B4 N8192
-// D1024 bf16: 55 us forward (3.7 TB/s), 99 us backward (4.1 TB/s); with checks
+// D1024 bf16: 51 us forward (3.9 TB/s), 92 us backward (4.4 TB/s); with checks
 // on every token, scalar arithmetic and a cluster barrier a round 73 and
-// 126 us; one thread a channel 9.8 ms for both.
+// 126 us; one thread a channel 9.8 ms for both.  A third stage in flight, or
+// 16-byte copies shared by two lanes, gain nothing.
 //
 // The CTAs of a cluster run at the same time, and each sends before it waits.
 // The totals' buffers alternate: a CTA sends those of round i + 2 only after it
@@ -121,10 +122,7 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 // its reads of round i.
 constexpr int kTile = 32;     // channels of a CTA
 constexpr int kStages = 2;
-#ifndef SCAN_MC
-#define SCAN_MC 8
-#endif
-constexpr int kMaxCluster = SCAN_MC;
+constexpr int kMaxCluster = 8;  // portable; 16 gain a tenth on few tiles and cost as much on many
 constexpr uint32_t kWait = 1u << 24;  // polls of a cluster's totals
 
 template <typename T, int V>
@@ -231,11 +229,12 @@ __device__ __forceinline__ void send(float2* mine, uint64_t* bar, int rank, floa
                  : "memory");
 }
 
-// Elements (tokens x channels) of a thread and chunk: 32 KB of tokens a stage,
-// which two CTAs of 128 registers a thread hold on an SM.  Half as many, at
-// three CTAs, cost a fifth more time: what a round costs whatever its length
-// (the joins, the wait for the cluster) counts twice as often.  Single bf16
-// channels, whose loads nothing runs ahead of, gain from the third CTA.
+// Elements (tokens x channels) of a thread and chunk: 128 bytes of tokens a
+// thread and stage, which sixteen warps of 128 registers a thread hold on an
+// SM.  Half as many, at twenty-four warps, cost a fifth more time: what a round
+// costs whatever its length (the joins, the wait for the cluster) counts twice
+// as often.  Single bf16 channels, whose loads nothing runs ahead of, gain from
+// the third part of warps (B4 N8192 D1023: 127 us, with sixteen 194).
 template <typename T, int V, bool BWD>
 constexpr bool kSingles = V * sizeof(T) < 4;
 template <typename T, int V, bool BWD>
@@ -533,7 +532,6 @@ cudaError_t launch_scan_w(const ScanArgs& a, cudaStream_t stream) {
         static std::atomic<uint64_t> done{0};
         const cudaError_t e = entry::allow_smem(kernel, (int)smem, done);
         if (e != cudaSuccess) return e;
-        if (SCAN_MC > 8) cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(work * cluster));

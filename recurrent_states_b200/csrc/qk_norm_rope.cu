@@ -517,6 +517,7 @@ qk_vec_kernel(const __grid_constant__ QkArgs a, int lpr, int tok, int slices, in
         }
         __syncthreads();  // cs is free for the next tile
     }
+    ptx::pdl_launch_dependents();
     if (BWD && a.dw) {  // the last barrier above stands between the sums and their readers
         for (int i = tid; i < 2 * a.d; i += 256) {
             const int z = i / a.d, e = i - z * a.d;
@@ -548,16 +549,26 @@ QkKernel<T, BWD> qk_vec(int ve, int lpr) {
     return qk_vec_kernel<T, 2, 0, BWD>;
 }
 
-// dw[z][c] = sum of the CTAs' partials, one warp per column, in a fixed order.
-__global__ void __launch_bounds__(256)
+// dw[z][c] = sum of the CTAs' partials, 32 columns a CTA: warp w takes every
+// 32nd partial sum from w on, then the warps' sums are joined, in this order.
+__global__ void __launch_bounds__(1024)
 qk_weight_grad_kernel(const float* __restrict__ part, int parts, int d, float* dqw, float* dkw) {
-    const int col = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (col >= 2 * d) return;
+    __shared__ float red[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+    ptx::pdl_wait_primary();
     float v = 0.f;
-    for (int i = lane; i < parts; i += 32) v += part[(int64_t)i * 2 * d + col];
-    v = warp_sum(v);
-    float* out = col < d ? dqw : dkw;
-    if (lane == 0 && out) out[col < d ? col : col - d] = v;
+    if (col < 2 * d) {
+#pragma unroll 8
+        for (int i = warp; i < parts; i += 32) v += part[(int64_t)i * 2 * d + col];
+    }
+    red[warp][lane] = v;
+    __syncthreads();
+    const int c = blockIdx.x * 32 + warp;
+    v = warp_sum(red[lane][warp]);
+    if (lane == 0 && c < 2 * d) {
+        float* out = c < d ? dqw : dkw;
+        if (out) out[c < d ? c : c - d] = v;
+    }
 }
 
 // Whether the rows can be moved in pieces of VE entries: their length, the
@@ -634,9 +645,10 @@ cudaError_t launch_qk(QkArgs& a, float* dqw, float* dkw, cudaStream_t stream) {
     cudaError_t e = cudaGetLastError();
     if (weights) {
         if (e == cudaSuccess) {
+            // its launch overlaps the end of the kernel before
             TA_TIMED(stream, "qk_weight_grad_kernel",
-                     qk_weight_grad_kernel<<<(2 * a.d + 7) / 8, 256, 0, stream>>>(a.dw, (int)grid, a.d, dqw, dkw));
-            e = cudaGetLastError();
+                     e = launch_maybe_pdl(qk_weight_grad_kernel, dim3((2 * a.d + 31) / 32), dim3(1024), 0, stream, true,
+                                          static_cast<const float*>(a.dw), (int)grid, a.d, dqw, dkw));
         }
         const cudaError_t f = workspace_free(a.dw, stream);
         if (e == cudaSuccess) e = f;
