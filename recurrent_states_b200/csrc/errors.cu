@@ -27,6 +27,7 @@ unsigned int* device_error_word() {
         return nullptr;
     }
     std::call_once(g_once[dev], [dev]() {
+        const RelaxedCapture relaxed;
         void* p = nullptr;
         if (cudaGetSymbolAddress(&p, g_error_word) != cudaSuccess) {
             cudaGetLastError();

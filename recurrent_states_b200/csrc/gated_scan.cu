@@ -25,8 +25,6 @@ namespace ta {
 
 namespace {
 
-constexpr unsigned int kErrScanWait = 16u;  // bit of the device error word
-
 struct ScanArgs {
     const void *gate, *x, *h, *dh;     // h, dh: backward
     const float *first, *last;         // the state before the first token, the last state's gradient; or NULL
@@ -106,12 +104,13 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 // So each input is read and each output written once, whatever the length.
 // The tokens arrive by asynchronous copies, two chunks deep, each thread's
 // into slots that it alone reads; only pieces under 4 bytes (single bf16
-// channels, where width or alignment is odd) are loaded directly.
+// channels, where width or alignment is odd) are loaded into registers, a round
+// ahead.
 //
 // Memory bounds the operator, 6 B a value forward and 12 B backward in bf16;
 // this kernel is bound by instructions and the latency of its rounds: 25 and
 // 49 instructions a value, issue slots 54 % taken at 14 warps an SM.  B4 N8192
-// D1024 bf16: 51 us forward (3.9 TB/s), 92 us backward (4.4 TB/s); with checks
+// D1024 bf16: 52 us forward (3.8 TB/s), 91 us backward (4.4 TB/s); with checks
 // on every token, scalar arithmetic and a cluster barrier a round 73 and
 // 126 us; one thread a channel 9.8 ms for both.  A third stage in flight, or
 // 16-byte copies shared by two lanes, gain nothing.
@@ -233,19 +232,17 @@ __device__ __forceinline__ void send(float2* mine, uint64_t* bar, int rank, floa
 // thread and stage, which sixteen warps of 128 registers a thread hold on an
 // SM.  Half as many, at twenty-four warps, cost a fifth more time: what a round
 // costs whatever its length (the joins, the wait for the cluster) counts twice
-// as often.  Single bf16 channels, whose loads nothing runs ahead of, gain from
-// the third part of warps (B4 N8192 D1023: 127 us, with sixteen 194).
-template <typename T, int V, bool BWD>
-constexpr bool kSingles = V * sizeof(T) < 4;
+// as often.  Single bf16 channels hold half as many, and the next round's
+// beside them (B4 N8192 D1023: 79 and 178 us; loaded in the round itself 127
+// and 277).
 template <typename T, int V, bool BWD>
 constexpr int elements() {
-    return 32 / (int)sizeof(T) / (BWD ? 2 : 1) * (kSingles<T, V, BWD> ? 1 : 2);
+    return 32 / (int)sizeof(T) / (BWD ? 2 : 1) * (V * sizeof(T) < 4 ? 1 : 2);
 }
-template <typename T, int V, bool BWD>
-constexpr int kSmWarps = kSingles<T, V, BWD> ? 24 : 16;  // warps an SM holds
+constexpr int kSmWarps = 16;  // warps an SM holds
 
 template <typename T, int V, bool BWD, int W>
-__global__ void __launch_bounds__(32 * W, kSmWarps<T, V, BWD> / W)
+__global__ void __launch_bounds__(32 * W, kSmWarps / W)
 scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int rounds, unsigned int* err) {
     constexpr int LC = kTile / V, GROUPS = 32 / LC;   // lanes of a token; token groups of a warp
     constexpr int R = elements<T, V, BWD>() / V;         // tokens of a thread
@@ -262,11 +259,21 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % cluster;
     const int tile = blockIdx.x / cluster % tiles, b = blockIdx.x / cluster / tiles;
-    const int d0 = tile * kTile, ch = lane % LC * V, d = d0 + ch;
-    const bool on = d < a.D;                          // V divides D where V > 1
+    const int d0 = tile * kTile;
+    // V divides D.  Lanes past the last channels compute what nobody uses: they
+    // fetch and write nothing (many copies of one word into as many slots take
+    // as many passes), their direct loads take the last channels
+    const int ch = lane % LC * V, d = min(d0 + ch, a.D - V);
+    const bool own = d == d0 + ch;
     const int len = a.lengths ? min(max(a.lengths[b], 0), a.N) : a.N;
     const int first = (warp * GROUPS + lane / LC) * R;  // of this thread's tokens in the chunk, in walking order
 
+    // lane l of every warp carries channel d0 + l of the state; read before the
+    // cluster's barrier, since the last state may be written over the first
+    const bool chan = d0 + lane < a.D;
+    const int64_t state = (int64_t)b * a.D + d0 + lane;
+    const float* init = BWD ? a.last : a.first;
+    float run = init && chan ? init[state] : 0.f;
     if (cluster > 1) {
         if (tid == 0) {
             ptx::mbar_init(&bars[0], 1);
@@ -278,11 +285,6 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
-    // lane l of every warp carries channel d0 + l of the state
-    const bool chan = d0 + lane < a.D;
-    const int64_t state = (int64_t)b * a.D + d0 + lane;
-    const float* init = BWD ? a.last : a.first;
-    float run = init && chan ? init[state] : 0.f;
     bool lost = false;  // a wait ran out
 
     const T* src[K];
@@ -300,13 +302,14 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         const unsigned s = ((unsigned)round * cluster + rank) * CT + first;  // past 2^31 in the last round at most
         return (int)(BWD ? (unsigned)a.N - 1u - s : s);
     };
-    // whether every token and channel of this CTA's chunk exists, and (backward) has one before it
+    // whether every token of this CTA's chunk exists, and (backward) has one
+    // before it
     auto whole = [&](int round) {
         const int64_t s = ((int64_t)round * cluster + rank) * CT;
-        return d0 + kTile <= a.D && (BWD ? a.N - s <= len && a.N - s - CT >= 1 : s + CT <= len);
+        return BWD ? a.N - s <= len && a.N - s - CT >= 1 : s + CT <= len;
     };
-    auto used = [&](int t, int k) { return on && t >= (k == 2 ? 1 : 0) && t < len; };
-    auto inside = [&](int t) { return on && (unsigned)t < (unsigned)a.N; };
+    auto used = [&](int t, int k) { return t >= (k == 2 ? 1 : 0) && t < len; };
+    auto inside = [&](int t) { return (unsigned)t < (unsigned)a.N; };
     auto fetch = [&](int round) {
         if constexpr (kAsync) {
             if (round < rounds) {
@@ -317,8 +320,10 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
                 for (int k = 0; k < K; ++k) {
                     const T* p = src[k] + t0 * step[k];
                     if (all) {
+                        if (own) {
 #pragma unroll
-                        for (int r = 0; r < R; ++r, p += DIR * step[k]) fetch_async<sizeof(Piece)>(to + (k * R + r) * kThreads, p);
+                            for (int r = 0; r < R; ++r, p += DIR * step[k]) fetch_async<sizeof(Piece)>(to + (k * R + r) * kThreads, p);
+                        }
                     } else {
 #pragma unroll
                         for (int r = 0; r < R; ++r, p += DIR * step[k])
@@ -329,6 +334,24 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
             ptx::cp_async_commit();
         }
     };
+    // single bf16 channels: the next round's, in registers
+    Piece next[kAsync ? 1 : K][kAsync ? 1 : R];
+    auto read = [&](int round) {
+        if constexpr (!kAsync) {
+            const int t0 = token(round);
+            const bool all = round < rounds && whole(round);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const T* p = src[k] + t0 * step[k];
+#pragma unroll
+                for (int r = 0; r < R; ++r, p += DIR * step[k]) {
+                    next[k][r] = Piece{};
+                    if (all || (round < rounds && used(t0 + DIR * r, k))) next[k][r] = *reinterpret_cast<const Piece*>(p);
+                }
+            }
+        }
+    };
+    read(0);
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
 
     for (int round = 0; round < rounds; ++round) {
@@ -340,7 +363,7 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         const Piece* mine = slots + (round % kStages) * K * R * kThreads + tid;
         auto piece = [&](int k, int r) {
             if constexpr (kAsync) return mine[(k * R + r) * kThreads];
-            else return *reinterpret_cast<const Piece*>(src[k] + (t0 + DIR * r) * step[k]);
+            else return next[k][r];
         };
         const bool all = whole(round);
         // 1. this thread's tokens: A and b of each, and their join
@@ -376,6 +399,12 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         };
         if (all) gather(std::true_type{});
         else gather(std::false_type{});
+        [[maybe_unused]] Piece kept[2][kAsync || !BWD ? 1 : R];  // x and h before, which are used again below
+        if constexpr (!kAsync && BWD) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) kept[0][r] = next[1][r], kept[1][r] = next[2][r];
+        }
+        read(round + 1);
         // 2. within the warp, over its token groups (by shuffles: through shared memory it
         // took 61 us instead of 55, B4 N8192 D1024 bf16)
         float ea[V], eb[V];
@@ -460,16 +489,20 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
                 if constexpr (!BWD) {
 #pragma unroll
                     for (int i = 0; i < P; ++i) s.e[i] = fma2(A[r].e[i], s.e[i], Bv[r].e[i]);
-                    if (every || inside(t)) *reinterpret_cast<Piece*>(y) = u ? pack<T, V>(s) : Piece{};
+                    if (own && (every || inside(t))) *reinterpret_cast<Piece*>(y) = u ? pack<T, V>(s) : Piece{};
                     y += a.D;
                 } else {
                     Piece px{}, ph{};
-                    if (u) px = piece(1, r);
-                    if (every || used(t, 2)) ph = piece(2, r);
+                    if constexpr (kAsync) {
+                        if (u) px = piece(1, r);
+                        if (every || used(t, 2)) ph = piece(2, r);
+                    } else {
+                        px = kept[0][r], ph = kept[1][r];
+                    }
                     Lanes<V> x, before, og, ox;
                     unpack(px, x);
                     unpack(ph, before);
-                    if (!every && t == 0 && a.first && on) {
+                    if (!every && t == 0 && a.first) {
                         float f[V];
 #pragma unroll
                         for (int v = 0; v < V; ++v) f[v] = a.first[(int64_t)b * a.D + d + v];
@@ -484,7 +517,7 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
                         og.e[i] = mul2(mul2(s.e[i], keep[r].e[i]), diff);
                         ox.e[i] = a.coupled ? mul2(G, keep[r].e[i]) : G;
                     }
-                    if (every || inside(t)) {
+                    if (own && (every || inside(t))) {
                         *reinterpret_cast<Piece*>(dg) = u ? pack<T, V>(og) : Piece{};
                         *reinterpret_cast<Piece*>(dx) = u ? pack<T, V>(ox) : Piece{};
                     }
@@ -519,7 +552,7 @@ cudaError_t launch_scan_w(const ScanArgs& a, cudaStream_t stream) {
     const int64_t chunks = (a.N + CT - 1) / CT;
     // CTAs that fit at once share a sequence while there are more of them than
     // channel tiles
-    int64_t cluster = (int64_t)entry::num_sms() * (kSmWarps<T, V, BWD> / W) / work;
+    int64_t cluster = (int64_t)entry::num_sms() * (kSmWarps / W) / work;
     if (cluster > chunks) cluster = chunks;
     if (cluster > kMaxCluster) cluster = kMaxCluster;
     if (cluster < 1) cluster = 1;
@@ -552,7 +585,7 @@ cudaError_t launch_scan_w(const ScanArgs& a, cudaStream_t stream) {
 
 // Four warps a CTA where its channel tiles, or the chunks of a short sequence,
 // make enough of them: four CTAs an SM wait for one another's joins less than
-// two of eight (B4 N8192 D1024 bf16: 51 and 92 us, with eight 54 and 99).
+// two of eight (B4 N8192 D1024 bf16: 52 and 91 us, with eight 54 and 99).
 // Eight where a cluster's size limits how many warps share a tile (B1 N65536
 // D512: 98 and 180 us, with four 113 and 195).
 template <typename T, int V, bool BWD>
@@ -579,8 +612,8 @@ gated_step_kernel(const T* __restrict__ gate, const T* __restrict__ x, const flo
     const int64_t total = (int64_t)B * per;
     for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int b = (int)(i / per), d = (int)(i - (int64_t)b * per) * VE;
-        T g[VE], v[VE], o[VE];
-        float s[VE];
+        alignas(16) T g[VE], v[VE], o[VE];
+        alignas(16) float s[VE];
         const int64_t at = (int64_t)b * D + d;
         if constexpr (VE == 4) {
             if constexpr (sizeof(T) == 2) {

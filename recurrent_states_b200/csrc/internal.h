@@ -22,6 +22,17 @@ void end(cudaStream_t s);
         ::ta::timing::end((stream));             \
     } while (0)
 
+// While it lives, this thread may make calls that set something up once per
+// device (a memory pool, a symbol's address) although a stream is being
+// captured; nothing that is captured depends on them.
+struct RelaxedCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    RelaxedCapture(const RelaxedCapture&) = delete;
+    RelaxedCapture& operator=(const RelaxedCapture&) = delete;
+};
+
 // Stream-ordered workspace from the library's per-device pool (workspace.cu).
 cudaError_t workspace_alloc(void** ptr, size_t bytes, cudaStream_t stream);
 cudaError_t workspace_free(void* ptr, cudaStream_t stream);
@@ -32,6 +43,8 @@ constexpr unsigned int kErrDecodeLoad = 1u;
 constexpr unsigned int kErrDecodeStore = 2u;
 constexpr unsigned int kErrPrefillPipe = 4u;
 constexpr unsigned int kErrSelfTest = 8u;
+constexpr unsigned int kErrScanWait = 16u;
+constexpr unsigned int kErrPrefixLength = 32u;
 
 template <typename Tin>
 cudaError_t launch_decode(const Tin* q, const Tin* k, const Tin* v, float* state, float* out,

@@ -98,28 +98,36 @@ __device__ __forceinline__ float far_norm(float (&x)[E], float s, float eps, flo
     return rsqrtf(s + eps);
 }
 
-// Any d: one warp per token and head slice, lane l holding the entries l and
-// l + 32, looping over the heads so that the angles are formed once.  Rows
-// are read and written element by element; the vector kernel below takes the
-// rows whose length and alignment allow wider accesses.
-template <typename T, bool BWD>
+// Any d: LPR neighbouring lanes per token and head slice, lane l holding entry
+// l (and l + 32 where E is 2: then one head at a time, four need too many
+// registers), walking the heads four at a time so that the angles are formed
+// once.  Rows are read and written element by element; the
+// vector kernel below takes the rows whose length and alignment allow wider
+// accesses.
+template <typename T, int LPR, int E, bool BWD>
 __global__ void __launch_bounds__(256)
 qk_any_kernel(const __grid_constant__ QkArgs a, int slices) {
     __shared__ float red[8][2][kMaxDk];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int PER = 32 / LPR, kAnyRows = E == 2 ? 1 : 4;  // tokens of a warp; heads in flight
+    const int l = lane & (LPR - 1), base = lane & ~(LPR - 1);
     const int half = a.rot >> 1;
-    const int64_t items = (int64_t)a.B * a.N * slices;
-    float acc[2][2] = {};
-    for (int64_t it = (int64_t)blockIdx.x * 8 + warp; it < items; it += (int64_t)gridDim.x * 8) {
+    const int64_t tokens = (int64_t)a.B * a.N, groups = (tokens + PER - 1) / PER;
+    float acc[2][E] = {};
+    for (int64_t it = (int64_t)blockIdx.x * 8 + warp; it < groups * slices; it += (int64_t)gridDim.x * 8) {
         const int slice = (int)(it % slices);
-        const unsigned t = (unsigned)(it / slices);
+        const int64_t at = it / slices * PER + base / LPR;
+        const bool live = at < tokens;
+        const unsigned t = live ? (unsigned)at : 0u;
         const int b = t / (unsigned)a.N, n = t - (unsigned)b * (unsigned)a.N;
         const int64_t p = a.pos ? a.pos[t] : a.pos0 + n;
-        float c[2], s[2];
-        int mate[2];
+        float c[E], s[E];
+        int mate[E];
+        bool on[E];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = lane + 32 * e;
+        for (int e = 0; e < E; ++e) {
+            const int i = l + 32 * e;
+            on[e] = live && i < a.d;
             c[e] = 1.f, s[e] = 0.f, mate[e] = i;
             if (i < a.rot) {
                 const bool first = a.inter ? (i & 1) == 0 : i < half;
@@ -131,48 +139,78 @@ qk_any_kernel(const __grid_constant__ QkArgs a, int slices) {
         }
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
-            const float* w = a.w[z];
-            const float w0 = w && lane < a.d ? w[lane] : 1.f, w1 = w && lane + 32 < a.d ? w[lane + 32] : 1.f;
-            for (int h = slice; h < a.H[z]; h += slices) {
-                const T* xr = static_cast<const T*>(a.x[z]) + b * a.xs[z][0] + n * a.xs[z][1] + h * a.xs[z][2];
-                const int64_t dense = (((int64_t)b * a.H[z] + h) * a.N + n) * a.d;
-                float x[2] = {lane < a.d ? to_float(xr[lane]) : 0.f,
-                              lane + 32 < a.d ? to_float(xr[lane + 32]) : 0.f};
-                float m;
-                const float inv = far_norm<2>(x, warp_sum(fmaf(x[0], x[0], x[1] * x[1])), a.eps, m, 32);
-                float in[2];
-                if (BWD) {
-                    const T* gr = static_cast<const T*>(a.dy[z]) + dense;
-                    in[0] = lane < a.d ? to_float(gr[lane]) : 0.f;
-                    in[1] = lane + 32 < a.d ? to_float(gr[lane + 32]) : 0.f;
-                } else {
-                    in[0] = x[0] * w0;
-                    in[1] = x[1] * w1;
-                }
-                float out[2];
+            float w[E];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float lo = __shfl_sync(0xffffffffu, in[0], mate[e] & 31);
-                    const float hi = __shfl_sync(0xffffffffu, in[1], mate[e] & 31);
-                    const float other = mate[e] & 32 ? hi : lo;
-                    out[e] = lane + 32 * e < a.rot ? fmaf(other, s[e], in[e] * c[e]) : in[e];
+            for (int e = 0; e < E; ++e) w[e] = a.w[z] && l + 32 * e < a.d ? a.w[z][l + 32 * e] : 1.f;
+            const T* xb = static_cast<const T*>(a.x[z]) + b * a.xs[z][0] + n * a.xs[z][1] + l;
+            const int64_t dense = ((int64_t)b * a.H[z] * a.N + n) * a.d + l, dense_h = (int64_t)a.N * a.d;
+            for (int h0 = slice; h0 < a.H[z]; h0 += kAnyRows * slices) {
+                float x[kAnyRows][E], in[kAnyRows][E], sq[kAnyRows];
+#pragma unroll
+                for (int u = 0; u < kAnyRows; ++u) {
+                    const int h = h0 + u * slices;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const bool use = on[e] && h < a.H[z];
+                        x[u][e] = use ? to_float(xb[h * a.xs[z][2] + 32 * e]) : 0.f;
+                        if (BWD) in[u][e] = use ? to_float(static_cast<const T*>(a.dy[z])[dense + h * dense_h + 32 * e]) : 0.f;
+                    }
                 }
-                if (BWD) {
-                    const float xh0 = x[0] * inv, xh1 = x[1] * inv;
-                    acc[z][0] = fmaf(out[0], xh0, acc[z][0]);
-                    acc[z][1] = fmaf(out[1], xh1, acc[z][1]);
-                    const float g0 = out[0] * w0, g1 = out[1] * w1;
-                    const float along = warp_sum(g0 * xh0 + g1 * xh1);
-                    T* o = static_cast<T*>(a.y[z]) + b * a.ys[z][0] + n * a.ys[z][1] + h * a.ys[z][2];
-                    out[0] = (g0 - xh0 * along) * inv;
-                    out[1] = (g1 - xh1 * along) * inv;
-                    if (m != 1.f) out[0] /= m, out[1] /= m;
-                    if (lane < a.d) o[lane] = from_float<T>(out[0]);
-                    if (lane + 32 < a.d) o[lane + 32] = from_float<T>(out[1]);
-                } else {
-                    T* o = static_cast<T*>(a.y[z]) + dense;
-                    if (lane < a.d) o[lane] = from_float<T>(out[0] * inv);
-                    if (lane + 32 < a.d) o[lane + 32] = from_float<T>(out[1] * inv);
+#pragma unroll
+                for (int u = 0; u < kAnyRows; ++u) {
+                    sq[u] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) sq[u] = fmaf(x[u][e], x[u][e], sq[u]);
+                }
+#pragma unroll
+                for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int u = 0; u < kAnyRows; ++u) sq[u] += __shfl_xor_sync(0xffffffffu, sq[u], o);
+#pragma unroll
+                for (int u = 0; u < kAnyRows; ++u) {
+                    const int h = h0 + u * slices;
+                    if (h >= a.H[z]) break;  // the same in all lanes
+                    float m;
+                    const float inv = far_norm<E>(x[u], live ? sq[u] : 1.f, a.eps, m, LPR);
+                    float out[E];
+                    if (!BWD) {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) in[u][e] = x[u][e] * w[e];
+                    }
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        const int from = base + (mate[e] & 31);
+                        float other = __shfl_sync(0xffffffffu, in[u][0], from);
+                        if constexpr (E == 2) {
+                            const float hi = __shfl_sync(0xffffffffu, in[u][1], from);
+                            other = mate[e] & 32 ? hi : other;
+                        }
+                        out[e] = fmaf(other, s[e], in[u][e] * c[e]);  // s is 0 past the rotation, other its own entry
+                    }
+                    if (BWD) {
+                        float along = 0.f;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            x[u][e] *= inv;
+                            acc[z][e] = fmaf(out[e], x[u][e], acc[z][e]);
+                            out[e] *= w[e];
+                            along = fmaf(out[e], x[u][e], along);
+                        }
+#pragma unroll
+                        for (int o = LPR / 2; o > 0; o >>= 1) along += __shfl_xor_sync(0xffffffffu, along, o);
+                        T* o = static_cast<T*>(a.y[z]) + b * a.ys[z][0] + n * a.ys[z][1] + h * a.ys[z][2] + l;
+#pragma unroll
+                        for (int e = 0; e < E; ++e) {
+                            out[e] = (out[e] - x[u][e] * along) * inv;
+                            if (m != 1.f) out[e] /= m;
+                            if (on[e]) o[32 * e] = from_float<T>(out[e]);
+                        }
+                    } else {
+                        T* o = static_cast<T*>(a.y[z]) + dense + h * dense_h;
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (on[e]) o[32 * e] = from_float<T>(out[e] * inv);
+                    }
                 }
             }
         }
@@ -181,7 +219,12 @@ qk_any_kernel(const __grid_constant__ QkArgs a, int slices) {
 #pragma unroll
         for (int z = 0; z < 2; ++z)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) red[warp][z][lane + 32 * e] = acc[z][e];
+            for (int e = 0; e < E; ++e) {
+                // the warp's tokens first
+#pragma unroll
+                for (int o = LPR; o < 32; o <<= 1) acc[z][e] += __shfl_xor_sync(0xffffffffu, acc[z][e], o);
+                if (base == 0) red[warp][z][l + 32 * e] = acc[z][e];
+            }
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * a.d; i += 256) {
             const int z = i / a.d, c = i - z * a.d;
@@ -190,6 +233,16 @@ qk_any_kernel(const __grid_constant__ QkArgs a, int slices) {
             a.dw[(int64_t)blockIdx.x * 2 * a.d + i] = v;
         }
     }
+}
+
+template <typename T, bool BWD>
+auto qk_any(int d) -> void (*)(QkArgs, int) {
+    if (d > 32) return qk_any_kernel<T, 32, 2, BWD>;
+    if (d > 16) return qk_any_kernel<T, 32, 1, BWD>;
+    if (d > 8) return qk_any_kernel<T, 16, 1, BWD>;
+    if (d > 4) return qk_any_kernel<T, 8, 1, BWD>;
+    if (d > 2) return qk_any_kernel<T, 4, 1, BWD>;
+    return qk_any_kernel<T, 2, 1, BWD>;
 }
 
 // A row's piece of VE entries as it lies in memory: 4, 8 or 16 bytes.
@@ -354,7 +407,7 @@ qk_vec_kernel(const __grid_constant__ QkArgs a, int lpr, int tok, int slices, in
 #pragma unroll
         for (int e = 0; e < VE; ++e) dw[0][tid][e] = dw[1][tid][e] = 0.f;
     }
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const unsigned t0 = (unsigned)tile * (unsigned)tok, t = t0 + tl;
         const bool live = t < tokens && c * VE < a.d;
         const int b = live ? t / (unsigned)a.N : 0, n = live ? t - (unsigned)b * (unsigned)a.N : 0;
@@ -602,10 +655,13 @@ QkPlan plan_qk(const QkArgs& a, bool weights) {
         if (in_pieces<T, BWD>(a, ve)) p.ve = ve;
     if (!p.ve) {
         // enough warps to fill the GPU before a warp takes several heads
+        p.lpr = 2;
+        while (p.lpr < 32 && p.lpr < a.d) p.lpr *= 2;
+        const int64_t groups = (tokens + 32 / p.lpr - 1) / (32 / p.lpr);
         p.slices = 1;
-        while (p.slices < heads && tokens * p.slices < (int64_t)sms * 32) p.slices *= 2;
+        while (p.slices < heads && groups * p.slices < (int64_t)sms * 16) p.slices *= 2;
         if (p.slices > heads) p.slices = heads;
-        p.grid = (tokens * p.slices + 7) / 8;
+        p.grid = (groups * p.slices + 7) / 8;
         if (p.grid > (int64_t)sms * 8) p.grid = (int64_t)sms * 8;
         return p;
     }
@@ -636,7 +692,7 @@ cudaError_t launch_qk(QkArgs& a, float* dqw, float* dkw, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     if (!p.ve) {
-        TA_TIMED(stream, "qk_any_kernel", qk_any_kernel<T, BWD><<<grid, 256, 0, stream>>>(a, p.slices));
+        TA_TIMED(stream, "qk_any_kernel", qk_any<T, BWD>(a.d)<<<grid, 256, 0, stream>>>(a, p.slices));
     } else {
         const int tiles = (int)(((int64_t)a.B * a.N + p.tok - 1) / p.tok);
         const QkKernel<T, BWD> kernel = qk_vec<T, BWD>(p.ve, p.lpr);

@@ -26,7 +26,6 @@ namespace ta {
 
 namespace {
 
-constexpr unsigned int kErrLength = 32u;  // bit of the device error word
 constexpr int kMaxSplits = 32;            // shares of the features
 
 struct PrefixArgs {
@@ -310,7 +309,7 @@ prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster)
         ptx::pdl_wait_primary();
         if (rank == 0)
             for (int c = tid; c < a.dv; c += THREADS) a.out[(int64_t)bh * a.dv + c] = nanf("");
-        if (rank == 0 && tid == 0) atomicOr(a.err, kErrLength);
+        if (rank == 0 && tid == 0) atomicOr(a.err, kErrPrefixLength);
         return;
     }
     f32x2 q[KE / 2];

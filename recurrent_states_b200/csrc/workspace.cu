@@ -27,6 +27,8 @@ std::mutex g_threshold_mutex;
 cudaError_t pool_for(int dev, cudaMemPool_t* out) {
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::call_once(g_once[dev], [dev]() {
+        // a first call inside a stream capture may create the pool too
+        const ta::RelaxedCapture relaxed;
         cudaMemPoolProps props = {};
         props.allocType = cudaMemAllocationTypePinned;
         props.handleTypes = cudaMemHandleTypeNone;

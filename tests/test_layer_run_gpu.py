@@ -3,6 +3,10 @@ recurrent layer feeds projections, queries and keys are normalised and rotated,
 the attention takes the whole prompt once, and a batch of sequences continues
 from it token by token; and the gradients of the recurrent layer and the norms
 chained through the projection."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -15,6 +19,7 @@ from tests.gpu_common import f64
 pytestmark = pytest.mark.gpu
 
 DEV = "cuda:0"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 TAU = 2.0
 
 
@@ -174,3 +179,32 @@ def test_two_streams_at_once(capture):
         torch.cuda.synchronize()
         for w, o in zip(want, got):
             assert all(torch.equal(x, y) for x, y in zip(w, o))
+
+
+FIRST = {
+    "norms": "TA.taylor_attn_qk_norm_rope_backward(q, q, o, o, TA.rope_freqs(64), q_weight=w)",
+    "scan": "TA.taylor_attn_gated_scan(g, g)",
+    "prefix": "TA.taylor_attn_shared_prefix_decode(r(2, 4, 64), r(2, 4, 64), r(2, 4, 64), state, kc, kc, lens, 3, 2.0)",
+}
+
+
+@pytest.mark.parametrize("name", FIRST)
+def test_a_process_may_make_its_first_call_inside_a_capture(name):
+    """The workspace pool and the error word are set up by the first call that needs them."""
+    code = f"""
+import torch
+from recurrent_states_b200 import taylor_attn as TA
+r = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+q, o, g, w = r(2, 40, 4, 64), r(2, 4, 40, 64), r(2, 900, 64), torch.ones(64, device="cuda")
+state = torch.ones(4, TA.taylor_attn_state_stride(64, 64, 3), device="cuda")
+kc, lens = r(2, 4, 9, 64), torch.tensor([3, 8], dtype=torch.int32, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = {FIRST[name]}
+graph.replay()
+torch.cuda.synchronize()
+out = out if isinstance(out, tuple) else (out,)
+assert all(torch.isfinite(t).all() for t in out if t is not None)
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0, done.stderr[-1500:]
