@@ -487,10 +487,10 @@ qk_vec_kernel(const __grid_constant__ QkArgs a, int lpr, int tok, int slices, in
             T* y = BWD ? static_cast<T*>(a.y[z]) + b * a.ys[z][0] + n * a.ys[z][1] + slice * a.ys[z][2] + c * VE
                        : static_cast<T*>(a.y[z]) + at[z];
             const int64_t ystep = BWD ? slices * a.ys[z][2] : gstep;
-            const int end = z ? rows : rq;
+            const int end = z ? rows : rq, heads = a.H[z];
 #pragma unroll 1
             for (int h = slice; r < end; ++r, h += slices, y += ystep) {
-                const bool on = live && h < a.H[z];
+                const bool on = live && h < heads;
                 ptx::cp_async_wait<D - 1>();
                 Piece<W> px = {}, pg = {};
                 if (on) {

@@ -218,6 +218,19 @@ def test_parts_and_steps_make_the_whole(dtype, D):
     assert torch.equal(state, keep) and torch.equal(new.to(out.dtype), out)
 
 
+@pytest.mark.parametrize("N,D", [(5000, 40), (700, 33)])
+def test_states_may_be_written_over_the_ones_read(N, D):
+    """h_last over h0 and dh0 over dh_last, with several CTAs to a sequence."""
+    gate, x, h0, dh, dl = _inputs("bf16", 2, N, D, seed=5)
+    h, last = TA.taylor_attn_gated_scan(gate, x, h0=h0, h_last=True)
+    dgate, dx, dh0 = TA.taylor_attn_gated_scan_backward(gate, x, h, dh, h0=h0, dh_last=dl, dh0=True)
+    state, carry = h0.clone(), dl.clone()
+    h2, _ = TA.taylor_attn_gated_scan(gate, x, h0=state, h_last=state)
+    dgate2, dx2, _ = TA.taylor_attn_gated_scan_backward(gate, x, h, dh, h0=h0, dh_last=carry, dh0=carry)
+    assert torch.equal(h, h2) and torch.equal(state, last)
+    assert torch.equal(dgate, dgate2) and torch.equal(dx, dx2) and torch.equal(carry, dh0)
+
+
 def test_uncoupled_step():
     gate, x, h0, *_ = _inputs("f32", 4, 1, 20, seed=2)
     h, last = SCAN["f32"](gate, x, coupled=False, h0=h0, h_last=True)

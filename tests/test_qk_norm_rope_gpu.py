@@ -198,6 +198,17 @@ def test_empty_calls():
     qo, ko = TA.taylor_attn_qk_norm_rope(q, k0, TA.rope_freqs(16))
     want, _ = TA.taylor_attn_qk_norm_rope(q, q, TA.rope_freqs(16))
     assert torch.equal(qo, want) and ko.numel() == 0
+    for d in (16, 7):   # keys alone, in pieces and element by element
+        k, none = torch.randn(2, 5, 3, d, device=DEV).bfloat16(), torch.empty((2, 5, 0, d), dtype=torch.bfloat16, device=DEV)
+        both = TA.taylor_attn_qk_norm_rope(k, k, TA.rope_freqs(d // 2 * 2))
+        qo, ko = TA.taylor_attn_qk_norm_rope(none, k, TA.rope_freqs(d // 2 * 2))
+        assert qo.numel() == 0 and torch.equal(ko, both[1])
+        w = torch.ones(d, device=DEV)
+        more = dict(q_weight=w, k_weight=w)
+        _, dk, dqw, dkw = TA.taylor_attn_qk_norm_rope_backward(none, k, qo, ko, TA.rope_freqs(d // 2 * 2), **more)
+        _, dk2, _, dkw2 = TA.taylor_attn_qk_norm_rope_backward(k, k, ko, ko, TA.rope_freqs(d // 2 * 2), **more)
+        assert torch.equal(dk, dk2) and (dqw == 0).all()
+        torch.testing.assert_close(dkw, dkw2, rtol=1e-5, atol=1e-5)
 
 
 def test_streams_graphs_and_repeats():
