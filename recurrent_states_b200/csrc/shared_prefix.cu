@@ -237,19 +237,20 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
 // order that depends on the sizes alone.
 //
 // The cache's bytes bound it: 64 sequences of 16 heads, d 64 and 64, up to
-// 1,024 own tokens (144 MB) take 45 us with the shared part beside them, 3.2
+// 1,024 own tokens (144 MB) take 40 us with the shared part beside them, 3.6
 // TB/s; tokens in registers 68 us, with selects on every token 55 us.  What is
 // left is the start and end of each CTA (2 to 4 us of some 15).
 constexpr int kUnroll = 2;  // tokens of eight lanes in a step
 
 // Bytes of a token that one lane keeps in shared memory, and the steps that
-// fit into 256 bytes a thread (two at least, four at most).
+// fit into 256 bytes a thread (two at least; three at most, so that seven CTAs
+// of four warps stay on an SM).
 template <typename T, int KV, int VV, int J>
 constexpr int kLaneBytes = (KV + J * VV) * (int)sizeof(T);
 template <typename T, int KV, int VV, int J>
 constexpr int ahead() {
     constexpr int fit = 256 / (kUnroll * kLaneBytes<T, KV, VV, J>);
-    return fit < 2 ? 2 : fit > 4 ? 4 : fit;
+    return fit < 2 ? 2 : fit > 3 ? 3 : fit;
 }
 
 template <typename T, int N>
@@ -292,7 +293,7 @@ __device__ __forceinline__ void cluster_barrier() {
 // KV: entries of k a lane reads at once (0: one by one, any d_k); VV: columns
 // of v it reads at once, J times.
 template <typename T, int KV, int VV, int J, int NW>
-__global__ void __launch_bounds__(32 * NW, J* VV <= 16 ? 24 / NW : 1)
+__global__ void __launch_bounds__(32 * NW, J * VV > 16 ? 1 : NW == 4 ? 7 : 3)
 prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster) {
     constexpr int KE = KV ? KV : kMaxDk / 8, THREADS = 32 * NW, TOKENS = 4 * NW * kUnroll;
     extern __shared__ __align__(16) unsigned char ring[];
@@ -585,9 +586,9 @@ cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
     splits = (all + steps - 1) / steps;
     // the own tokens: four warps a sequence and head where there are many and
     // none is long (more CTAs stay in flight while some begin and others end:
-    // 1,024 heads of up to 512 tokens, d 16, 19.8 us, at eight warps 22.4; 4,096
-    // of up to 512, d 64, 91 and 99 us), else eight (a long one would still run
-    // when the others are done: 1,024 of up to 1,024, d 64, 48 and 45 us), and
+    // 1,024 heads of up to 512 tokens, d 16, 17.0 us, at eight warps 19; 4,096 of
+    // up to 512, d 64, 90 and 99 us), else eight (a long one would still run
+    // when the others are done: 1,024 of up to 1,024, d 64, 44 and 39 us), and
     // while that leaves each 256 tokens a cluster of CTAs
     const int64_t heads = (int64_t)a.B * a.H;
     const bool many = heads >= 2 * (int64_t)sms && (int64_t)a.cap * (a.d + a.dv) * (int64_t)sizeof(T) <= 192 * 1024;

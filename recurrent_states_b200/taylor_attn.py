@@ -489,11 +489,13 @@ def _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, 
     _want(dq_out, "dq_out", dtype, dev, (B, Hq, N, d))
     _want(dk_out, "dk_out", dtype, dev, (B, Hk, N, d))
     if dq is None:
-        dq = q.new_empty(B, N, Hq, d)
+        dq, dqs = q.new_empty(B, N, Hq, d), (N * Hq * d, Hq * d, d)
+    else:
+        dqs = _rows(dq, "dq", dtype, dev, q.shape)
     if dk is None:
-        dk = k.new_empty(B, N, Hk, d)
-    dqs = _rows(dq, "dq", dtype, dev, q.shape)
-    dks = _rows(dk, "dk", dtype, dev, k.shape)
+        dk, dks = k.new_empty(B, N, Hk, d), (N * Hk * d, Hk * d, d)
+    else:
+        dks = _rows(dk, "dk", dtype, dev, k.shape)
     dqw = None if q_weight is None else torch.empty_like(q_weight)
     dkw = None if k_weight is None else torch.empty_like(k_weight)
     rc = getattr(lib(), name)(q.data_ptr(), k.data_ptr(), dq_out.data_ptr(), dk_out.data_ptr(), _ptr(q_weight),
@@ -584,12 +586,15 @@ def _gated_scan_backward(name, dtype, gate, x, h, dh, coupled, h0, lengths, dh_l
     _want(dh, "dh", dtype, dev, (B, N, D))
     if dh_last is not None:
         _want(dh_last, "dh_last", torch.float32, dev, (B, D))
+    dgs = dxs = (N * D, D)
     if dgate is None:
         dgate = torch.empty_like(dh)
+    else:
+        dgs = _rows(dgate, "dgate", dtype, dev, gate.shape)
     if dx is None:
         dx = torch.empty_like(dh)
-    dgs = _rows(dgate, "dgate", dtype, dev, gate.shape)
-    dxs = _rows(dx, "dx", dtype, dev, gate.shape)
+    else:
+        dxs = _rows(dx, "dx", dtype, dev, gate.shape)
     if dh0 is True:
         dh0 = torch.empty((B, D), dtype=torch.float32, device=gate.device) if dh_last is None else torch.empty_like(dh_last)
     elif dh0 is False:
