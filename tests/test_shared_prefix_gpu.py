@@ -2,8 +2,9 @@
 
 Tolerance.  y is a sum of products: over F features phi_f(q) S_f, over L + 1
 own tokens K(tau q.k_j) v_j.  phi is a product of at most 4 entries and a
-weight (6 roundings), K a polynomial of degree 4 in a dot product of at most 64
-terms; sums run over at most F + L + 1 terms in strips and trees of which no
+weight (6 roundings), both of its product's factors are held as two tf32 parts
+(within 2^-21 = 8 u each, by truncation, and lo lo left out, 4 u), K a
+polynomial of degree 4 in a dot product of at most 64 terms; sums run over at most F + L + 1 terms in strips and trees of which no
 chain is longer than (F + L) / 8 + 64.  With A the sum of the terms' absolute
 values (for K the polynomial of |q|.|k|) and u = 2^-24 the numerator and the
 denominator are within (96 + (F + L) / 8) u A of theirs, and the quotient adds
