@@ -69,22 +69,29 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
+// Whether t = sum x^2 + eps is out of fp32's comfortable range, or NaN.  Above
+// 1e-30 the squares that underflow in the sum are nothing beside t, be it the
+// row's or eps that makes it so large.
+__device__ __forceinline__ bool out_of_range(float t) { return !(t > 1e-30f && t < 1e37f); }
+
 // 1 / sqrt(sum x^2 + eps) of rows held by groups of `lanes` neighbouring lanes,
-// from a lane's entries x and the group's sum of squares s.  Where s leaves
-// fp32's comfortable range, x is first divided by its largest entry m, and the
-// result belongs to x / m (m is returned, else 1).  A row of zeros with eps 0
-// gives 0: its output and its gradient are zero.  All 32 lanes call it
-// together.
+// from a lane's entries x and the group's sum of squares s.  Where s + eps is
+// out of range, x is first divided by m, the larger of its largest entry and
+// sqrt(eps), so that neither x / m nor eps / m^2 is above 1, and the result
+// belongs to x / m (m is returned, else 1).  A row of zeros with eps 0 gives 0:
+// its output and its gradient are zero.  All 32 lanes call it together.
 template <int E>
 __device__ __forceinline__ float far_norm(float (&x)[E], float s, float eps, float& m, int lanes) {
     m = 1.f;
-    const bool far = !(s > 1e-30f && s < 1e37f);
+    const float t = s + eps;
+    const bool far = out_of_range(t);
     if (__any_sync(0xffffffffu, far)) {
         float big = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) big = fmaxf(big, fabsf(x[e]));
         for (int o = lanes >> 1; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        if (far && s == s && big > 0.f && big < INFINITY) m = big;
+        const float size = fmaxf(big, sqrtf(eps));
+        if (far && t == t && size > 0.f && big < INFINITY) m = size;
         float s2 = 0.f;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -92,10 +99,10 @@ __device__ __forceinline__ float far_norm(float (&x)[E], float s, float eps, flo
             s2 = fmaf(x[e], x[e], s2);
         }
         for (int o = lanes >> 1; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
-        s = s2 + (m != 1.f && eps > 0.f ? eps / m / m : eps);
+        s = s2 + (m != 1.f ? eps / m / m : eps);
         return s != 0.f ? rsqrtf(s) : 0.f;
     }
-    return rsqrtf(s + eps);
+    return rsqrtf(t);
 }
 
 // Any d: LPR neighbouring lanes per token and head slice, lane l holding entry
@@ -312,11 +319,12 @@ __device__ __forceinline__ float row_sum(float v, int lanes) {
     return v;
 }
 
-// Where a row's sum of squares s leaves fp32's comfortable range, scales the
-// row by a power of two to a largest entry in [1, 2) (exactly, but for entries
-// that are nothing beside it); the returned norm is that of the scaled row.  A
-// row of zeros with eps 0 has the norm's inverse 0, one with infinities or NaN
-// is left as it is.  Out of line: rows of ordinary size never come here.
+// Where t = sum x^2 + eps of a row is out of range, scales the row by a power
+// of two that takes the larger of its largest entry and sqrt(eps) to [1, 2)
+// (exactly, but for entries that are nothing beside it), and eps by its square;
+// the returned norm is that of the scaled row.  A row of zeros with eps 0 has
+// the norm's inverse 0, one with infinities or NaN is left as it is.  Out of
+// line: rows of ordinary size never come here.
 template <int W>
 struct Rescaled {
     Piece<W> row;
@@ -324,7 +332,7 @@ struct Rescaled {
     int by;  // the row was multiplied by 2^-by
 };
 template <typename T, int VE>
-__device__ __noinline__ Rescaled<VE * (int)sizeof(T) / 4> rescale(Piece<VE * (int)sizeof(T) / 4> r, float s, float eps,
+__device__ __noinline__ Rescaled<VE * (int)sizeof(T) / 4> rescale(Piece<VE * (int)sizeof(T) / 4> r, float t, float eps,
                                                                   int lanes) {
     f32x2 x[VE / 2];
     unpack<T, VE>(r, x);
@@ -335,8 +343,9 @@ __device__ __noinline__ Rescaled<VE * (int)sizeof(T) / 4> rescale(Piece<VE * (in
         big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
     }
     for (int o = lanes >> 1; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-    const bool far = !(s > 1e-30f && s < 1e37f) && s == s && big > 0.f && big < INFINITY;
-    const int by = far ? ilogbf(big) : 0;
+    const float size = fmaxf(big, sqrtf(eps));
+    const bool far = out_of_range(t) && t == t && size > 0.f && big < INFINITY;
+    const int by = far ? ilogbf(size) : 0;
     float s2 = 0.f;
 #pragma unroll
     for (int e = 0; e < VE / 2; ++e) {
@@ -349,11 +358,9 @@ __device__ __noinline__ Rescaled<VE * (int)sizeof(T) / 4> rescale(Piece<VE * (in
     for (int o = lanes >> 1; o > 0; o >>= 1) s2 += __shfl_xor_sync(0xffffffffu, s2, o);
     if (far) {
         r = pack<T, VE>(x);
-        s = s2;
-        eps = ldexpf(eps, -2 * by);
+        t = s2 + ldexpf(eps, -2 * by);
     }
-    s += eps;
-    return {r, s == 0.f ? 0.f : rsqrtf(s), by};
+    return {r, t == 0.f ? 0.f : rsqrtf(t), by};
 }
 
 constexpr int kDepth = 4;  // pieces a thread has in flight: four rows forward, two backward (x and dy)
@@ -503,13 +510,13 @@ qk_vec_kernel(const __grid_constant__ QkArgs a, int lpr, int tok, int slices, in
                 f32x2 sq = mul2(x[0], x[0]);
 #pragma unroll
                 for (int e = 1; e < P; ++e) sq = fma2(x[e], x[e], sq);
-                const float s = row_sum<LPR>(total2(sq), lpr);
+                const float norm2 = row_sum<LPR>(total2(sq), lpr) + a.eps;
                 float inv;
-                asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(on ? s + a.eps : 1.f));
+                asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(on ? norm2 : 1.f));
                 int by = 0;
-                const bool any = __any_sync(0xffffffffu, on && !(s > 1e-30f && s < 1e37f));
+                const bool any = __any_sync(0xffffffffu, on && out_of_range(norm2));
                 if (any) {
-                    const Rescaled<W> q = rescale<T, VE>(px, s, a.eps, lpr);
+                    const Rescaled<W> q = rescale<T, VE>(px, norm2, a.eps, lpr);
                     if (on) px = q.row, inv = q.inv, by = q.by;
                     unpack<T, VE>(px, x);
                 }

@@ -158,6 +158,51 @@ def test_rows_of_zeros_and_of_extreme_size(dtype, d):
     _check_backward(dk[:, 5:], None, k[:, 5:], dko[:, :, 5:], freqs, p[:, 5:], None, False, 0.0, dtype)
 
 
+# The size of a row, and eps beside it: eps that outweighs the row, that is of its order, and that is nothing beside it;
+# squares that leave fp32's range in either direction, and an eps that does so too.  Gradients stay inside the types'
+# range: dy / |x| at most 1e31.  Beside eps 1e38 a row of 1e-20 has outputs of 1e-39, below the types' normal numbers,
+# where a half step is h = 2^-150 in fp32 and 2^-134 in bf16 whatever the value: the row scaled by sqrt(eps) is rounded
+# to its type and enters as two entries times cosine, sine and weight (sqrt(2) max|w| h), the output is rounded (h).
+EXTREME = [(0.0, [1e-30, 1e-22, 1e-16, 1e19, 1e30, 1.0]),
+           (1e-6, [1e-22, 1e-23, 1e-24, 1e-30, 1e-36, 1e-4, 1e20]),
+           (1e-5, [1e-25, 1e-33, 1e-18, 1e-2]),
+           (1.0, [1e-20, 1e-21, 1e-36, 1e18, 1e30]),
+           (1e-31, [1e-24, 1e-17, 1e-15, 1e-12, 1e-36]),
+           (1e-38, [1e-19, 1e-20, 1e-30, 1e-36, 1.0]),
+           (1e38, [1e-20, 1.0, 1e18, 1e19, 1e24])]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,inter", [(16, False), (64, True), (20, False), (13, False), (41, True)])
+@pytest.mark.parametrize("eps,scales", EXTREME)
+def test_rows_of_extreme_size_with_and_without_eps(dtype, d, inter, eps, scales):
+    """Outputs and every row's gradient, weights' gradients among them, for rows in pieces and element by element."""
+    N = len(scales) + 2
+    q, k, dqo, dko, (qw, kw), pos = _inputs(dtype, 2, N, 2, 3, d, seed=d)
+    for x in (q, k):
+        for i, s in enumerate(scales):
+            x[0, i, 1] = (x[0, i, 1].double() * s).to(x.dtype)
+            x[1, i + 1] = (x[1, i + 1].double() * s).to(x.dtype)
+        x[1, 0, 0] = 0
+    freqs, p, eps32 = TA.rope_freqs(d // 2 * 2), pos.cpu().numpy(), float(np.float32(eps))
+    more = dict(positions=pos, q_weight=qw, k_weight=kw, interleaved=inter, eps=eps)
+    qo, ko = FORWARD[dtype](q, k, freqs, **more)
+    h = 2.0 ** -134 if dtype == "bf16" else 2.0 ** -150
+    for got, x, w in ((qo, q, qw), (ko, k, kw)):
+        want = L.norm_rope(f64(x), freqs, p, f64(w), inter, eps32)
+        limit = 64 * U * 2 ** 0.5 * np.abs(want).max(-1, keepdims=True) + (1 + 2 ** 0.5 * float(w.abs().max())) * h
+        if dtype == "bf16":
+            limit = limit + _half(dtype) * np.abs(want) * (1 + 1e-3)
+        assert (np.abs(f64(got) - want) <= limit).all(), float((np.abs(f64(got) - want) / limit).max())
+    dq, dk, dqw, dkw = BACKWARD[dtype](q, k, dqo, dko, freqs, **more)
+    _check_backward(dq, dqw, q, dqo, freqs, p, qw, inter, eps32, dtype)
+    _check_backward(dk, dkw, k, dko, freqs, p, kw, inter, eps32, dtype)
+    plain = dict(positions=pos, interleaved=inter, eps=eps)
+    dq, dk, _, _ = BACKWARD[dtype](q, k, dqo, dko, freqs, **plain)
+    _check_backward(dq, None, q, dqo, freqs, p, None, inter, eps32, dtype)
+    _check_backward(dk, None, k, dko, freqs, p, None, inter, eps32, dtype)
+
+
 def test_gradients_into_slices_of_a_packed_gradient():
     B, N, H, d = 2, 21, 4, 16
     q, k, dqo, dko, (qw, kw), pos = _inputs("bf16", B, N, H, H, d, seed=8)
