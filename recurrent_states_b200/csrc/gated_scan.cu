@@ -228,6 +228,26 @@ __device__ __forceinline__ void send(float2* mine, uint64_t* bar, int rank, floa
                  : "memory");
 }
 
+// Waits for the totals of one parity.  The stores that complete the barrier
+// come from other CTAs and release at the cluster's scope, which is where they
+// have to be acquired.
+__device__ __forceinline__ bool totals_here(uint64_t* bar, uint32_t phase) {
+    for (uint32_t i = 0; i < kWait; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n"
+            "  .reg .pred p;\n"
+            "  mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            "  selp.u32 %0, 1, 0, p;\n"
+            "}\n"
+            : "=r"(ok)
+            : "r"(ptx::smem_u32(bar)), "r"(phase)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+
 // Elements (tokens x channels) of a thread and chunk: 128 bytes of tokens a
 // thread and stage, which sixteen warps of 128 registers a thread hold on an
 // SM.  Half as many, at twenty-four warps, cost a fifth more time: what a round
@@ -285,7 +305,7 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
-    bool lost = false;  // a wait ran out
+    bool lost = false;  // a wait of this thread ran out
 
     const T* src[K];
     int64_t step[K];
@@ -441,7 +461,7 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
             float2 before[W - 1];
 #pragma unroll
             for (int w = 0; w < W - 1; ++w) before[w] = w < warp ? warps[par][w][lane] : make_float2(1.f, 0.f);
-            if (!lost && !ptx::mbar_wait(&bars[par], (round >> 1) & 1, kWait)) {
+            if (!lost && !totals_here(&bars[par], (round >> 1) & 1)) {
                 // never in a sound run: the outputs from here on are not to be used
                 lost = true;
                 if (lane == 0) atomicOr(err, kErrScanWait);

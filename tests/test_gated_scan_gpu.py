@@ -147,6 +147,36 @@ def test_many_tiles_fill_the_gpu_more_than_once(dtype):
     _check_all(dtype, gate, x, h0, dh, dl, True, lengths, h, last, dgate, dx, dh0)
 
 
+# Channel tiles enough for CTAs of four warps, few enough that several of them share a sequence, and several rounds of
+# each cluster: the shapes of a training step.  Clusters of 4, of 6 (a last round of which some chunks are empty, ragged
+# lengths) and of 6 at an odd width.
+TRAINING = [
+    # B, N, D, coupled, lengths
+    (4, 1500, 1024, True, None),
+    (3, 1300, 1000, False, [1300, 771, 1]),
+    (3, 1100, 999, True, [640, 1100, 1099]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,D,coupled,lengths", TRAINING)
+def test_training_shapes_match_the_oracle(dtype, B, N, D, coupled, lengths):
+    """Forward, gradient, and both again with the states written over the ones read."""
+    gate, x, h0, dh, dl = _inputs(dtype, B, N, D, seed=D)
+    lens = None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    more = dict(coupled=coupled, lengths=lens)
+    TA.taylor_attn_device_errors(clear=True)
+    h, last = SCAN[dtype](gate, x, h0=h0, h_last=True, **more)
+    dgate, dx, dh0 = BACK[dtype](gate, x, h, dh, h0=h0, dh_last=dl, dh0=True, **more)
+    _check_all(dtype, gate, x, h0, dh, dl, coupled, lengths, h, last, dgate, dx, dh0)
+    state, carry = h0.clone(), dl.clone()
+    h2, _ = SCAN[dtype](gate, x, h0=state, h_last=state, **more)
+    dgate2, dx2, _ = BACK[dtype](gate, x, h, dh, h0=h0, dh_last=carry, dh0=carry, **more)
+    assert torch.equal(h, h2) and torch.equal(state, last)
+    assert torch.equal(dgate, dgate2) and torch.equal(dx, dx2) and torch.equal(carry, dh0)
+    assert TA.taylor_attn_device_errors() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("D", [64, 33])
 def test_padding_is_never_read(dtype, D):
