@@ -118,7 +118,10 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 // The CTAs of a cluster run at the same time, and each sends before it waits.
 // The totals' buffers alternate: a CTA sends those of round i + 2 only after it
 // has those of round i + 1, which every CTA sends after a CTA barrier behind
-// its reads of round i.
+// its reads of round i.  A CTA whose wait ran out (never in a sound run) takes
+// no further part in the exchange, sets the error word and walks on without
+// waiting; it stays until the others are through, since they may still send
+// to it.
 constexpr int kTile = 32;     // channels of a CTA
 constexpr int kStages = 2;
 constexpr int kMaxCluster = 8;  // portable; 16 gain a tenth on few tiles and cost as much on many
@@ -376,7 +379,7 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
 
     for (int round = 0; round < rounds; ++round) {
         const int par = round & 1;
-        if (cluster > 1 && tid == 0) ptx::mbar_arrive_expect_tx(&bars[par], cluster * kTile * 8);
+        if (cluster > 1 && tid == 0 && !lost) ptx::mbar_arrive_expect_tx(&bars[par], cluster * kTile * 8);
         fetch(round + kStages - 1);
         ptx::cp_async_wait<kStages - 1>();
         const int t0 = token(round);
@@ -449,7 +452,7 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         // across warps and CTAs, lane l for channel l: c is the state before this warp's tokens
         float c = run;
         if (cluster > 1) {
-            if (warp == 0) {
+            if (warp == 0 && !lost) {
                 float2 total = warps[par][0][lane];
 #pragma unroll
                 for (int w = 1; w < W; ++w) {
@@ -462,8 +465,7 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
 #pragma unroll
             for (int w = 0; w < W - 1; ++w) before[w] = w < warp ? warps[par][w][lane] : make_float2(1.f, 0.f);
             if (!lost && !totals_here(&bars[par], (round >> 1) & 1)) {
-                // never in a sound run: the outputs from here on are not to be used
-                lost = true;
+                lost = true;  // the outputs from here on are not to be used
                 if (lane == 0) atomicOr(err, kErrScanWait);
             }
             for (int i = 0; i < cluster; ++i) {
@@ -550,6 +552,10 @@ scan_kernel(const __grid_constant__ ScanArgs a, int tiles, int cluster, int roun
         else write(std::false_type{});
     }
     if (a.end && rank == 0 && warp == 0 && chan) a.end[state] = run;
+    if (lost) {  // until every thread of the cluster is here or gone
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+    }
 }
 
 template <typename T, bool BWD>
