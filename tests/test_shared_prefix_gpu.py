@@ -104,6 +104,31 @@ def test_decode_matches_the_oracle_and_appends(dtype, B, H, d, dv, n, cap, lengt
     assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
 
 
+# Enough heads of short caches for CTAs of four warps, at every way of reading keys (rows of 64, 32 and 16 entries, and
+# any other) and every count of a lane's columns; and shares of more than 256 features, whose descriptors are formed
+# several times, with the last group of features not a whole one (F 4,845, 2,145 and 6,545).
+MANY = [(19, 16, d, dv, 3, 40, [(i * 7) % 40 for i in range(19)]) for d in (64, 32, 16, 20) for dv in (20, 64, 100, 128, 256)]
+LARGE_SHARES = [
+    (17, 8, 16, 64, 5, 30, [(i * 11) % 30 for i in range(17)]),
+    (3, 32, 64, 64, 3, 6, [5, 0, 3]),
+    (70, 16, 64, 64, 3, 3, [i % 3 for i in range(70)]),
+    (4, 16, 32, 36, 4, 5, [4, 0, 1, 2]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,H,d,dv,n,cap,lengths", MANY + LARGE_SHARES)
+def test_many_heads_and_large_shares(dtype, B, H, d, dv, n, cap, lengths):
+    q, k, v, state, kc, vc, lens = _inputs(dtype, B, H, d, dv, n, cap, lengths, seed=d + dv)
+    before = kc.clone(), vc.clone()
+    out = DECODE[dtype](q, k, v, state, kc, vc, lens, n, TAU)
+    _check(out, q, k, v, state, *before, lens, n)
+    rows = torch.arange(B, device=DEV)
+    before[0][rows, :, lens.long()] = k
+    before[1][rows, :, lens.long()] = v
+    assert torch.equal(kc, before[0]) and torch.equal(vc, before[1])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d,dv", [(16, 64), (9, 20)])
 def test_rows_behind_a_sequence_are_never_read(dtype, d, dv):
