@@ -244,13 +244,28 @@ constexpr int kUnroll = 2;  // tokens of eight lanes in a step
 
 // Bytes of a token that one lane keeps in shared memory, and the steps that
 // fit into 256 bytes a thread (two at least; three at most, so that seven CTAs
-// of four warps stay on an SM).
+// of four warps stay on an SM where a lane keeps 32 bytes or less).
 template <typename T, int KV, int VV, int J>
 constexpr int kLaneBytes = (KV + J * VV) * (int)sizeof(T);
 template <typename T, int KV, int VV, int J>
 constexpr int ahead() {
     constexpr int fit = 256 / (kUnroll * kLaneBytes<T, KV, VV, J>);
     return fit < 2 ? 2 : fit > 3 ? 3 : fit;
+}
+
+// CTAs of NW warps that the compiler is to leave registers for on an SM: seven
+// of four warps or three of eight, one where a lane's 32 columns and more need
+// them, and no more than fit into 228 KB with their rings, sums (below) and the
+// 1 KB that each CTA costs.  fp32, d_v 128 lets four to six CTAs of four warps
+// in; held to seven's 72 registers it took 22.6 us (64 sequences of 16 heads, d
+// 20, up to 200 tokens) and 23.8 us (d 64), with 86 and 96 registers 21.6 and
+// 23.5 us.
+template <typename T, int KV, int VV, int J, int NW>
+constexpr int resident() {
+    constexpr int sums = (NW * (kMaxDv + 4) + kMaxDv + 1) * (int)sizeof(float);
+    constexpr int ring = 32 * NW * kUnroll * ahead<T, KV, VV, J>() * kLaneBytes<T, KV, VV, J>;
+    constexpr int fit = 228 * 1024 / (ring + sums + 1024), want = J * VV > 16 ? 1 : NW == 4 ? 7 : 3;
+    return fit < want ? fit : want;
 }
 
 template <typename T, int N>
@@ -293,7 +308,7 @@ __device__ __forceinline__ void cluster_barrier() {
 // KV: entries of k a lane reads at once (0: one by one, any d_k); VV: columns
 // of v it reads at once, J times.
 template <typename T, int KV, int VV, int J, int NW>
-__global__ void __launch_bounds__(32 * NW, J * VV > 16 ? 1 : NW == 4 ? 7 : 3)
+__global__ void __launch_bounds__(32 * NW, resident<T, KV, VV, J, NW>())
 prefix_own_kernel(const __grid_constant__ PrefixArgs a, int splits, int cluster) {
     constexpr int KE = KV ? KV : kMaxDk / 8, THREADS = 32 * NW, TOKENS = 4 * NW * kUnroll;
     extern __shared__ __align__(16) unsigned char ring[];
