@@ -455,8 +455,10 @@ qk_vec_kernel(const __grid_constant__ QkArgs a, int lpr, int tok, int slices, in
             const unsigned n0 = t0 % (unsigned)a.N;
             for (int ti = tid / hp; ti < tok; ti += 256 / hp) {
                 const unsigned ta = t0 + ti, na = n0 + ti;
-                if (j < half && ta < tokens) {
-                    const float2 v = cos_sin(a, a.pos ? a.pos[ta] : a.pos0 + (na < a.N ? na : na % (unsigned)a.N), j);
+                if (j < half) {
+                    // tokens past the last one: rows of zeros, whose sums an angle that is not a number would spoil
+                    float2 v = make_float2(1.f, 0.f);
+                    if (ta < tokens) v = cos_sin(a, a.pos ? a.pos[ta] : a.pos0 + (na < a.N ? na : na % (unsigned)a.N), j);
                     cs[0][ti * half + j] = v.x;
                     cs[1][ti * half + j] = v.y;
                 }

@@ -203,6 +203,22 @@ def test_rows_of_extreme_size_with_and_without_eps(dtype, d, inter, eps, scales)
     _check_backward(dk, None, k, dko, freqs, p, None, inter, eps32, dtype)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d,rot,inter", [(16, 16, False), (16, 16, True), (64, 64, False), (24, 14, True), (34, 34, False)])
+def test_tokens_that_do_not_exist_leave_the_weight_gradients_alone(dtype, d, rot, inter):
+    """A few tokens fill a part of a CTA; the rest of its angles' places hold what the call before left there: NaN, from
+    frequencies whose angles overflow."""
+    q, k, dqo, dko, (qw, kw), pos = _inputs(dtype, 1, 3, 1, 2, d, seed=d)
+    many = _inputs(dtype, 4, 4096, 1, 2, d, seed=1)
+    freqs, p = TA.rope_freqs(rot), pos.cpu().numpy()
+    for _ in range(3):
+        bad = BACKWARD[dtype](*many[:4], np.full(rot // 2, 1e308), pos0=1 << 40, q_weight=qw, k_weight=kw, interleaved=inter)
+        assert torch.isnan(bad[0]).any()
+        dq, dk, dqw, dkw = BACKWARD[dtype](q, k, dqo, dko, freqs, positions=pos, q_weight=qw, k_weight=kw, interleaved=inter)
+        _check_backward(dq, dqw, q, dqo, freqs, p, qw, inter, 0.0, dtype)
+        _check_backward(dk, dkw, k, dko, freqs, p, kw, inter, 0.0, dtype)
+
+
 def test_gradients_into_slices_of_a_packed_gradient():
     B, N, H, d = 2, 21, 4, 16
     q, k, dqo, dko, (qw, kw), pos = _inputs("bf16", B, N, H, H, d, seed=8)
