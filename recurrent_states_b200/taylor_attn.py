@@ -163,6 +163,12 @@ _current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _fits(name: str, *sizes: int) -> None:
+    """Refuses sizes that are no C int: ctypes would cut them to their low 32 bits."""
+    if max(sizes) > 0x7fffffff:
+        raise TaylorAttnError(TAYLOR_ERR_UNSUPPORTED, name)
+
+
 def _want(t: torch.Tensor, name: str, dtype, dev: int, shape) -> None:
     """_need against a device's index; the checks in their quickest form."""
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
@@ -445,6 +451,7 @@ def _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight,
             return _qk_norm_rope(name, dtype, q, k, freqs, positions, pos0, q_weight, k_weight, interleaved, eps,
                                  q_out, k_out, None)
     B, N, Hq, Hk, d, dev, qs, ks, rot, table = _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype)
+    _fits(name, B, N, Hq, Hk, d, rot)
     if q_out is None:
         q_out = q.new_empty(B, Hq, N, d)
     else:
@@ -486,6 +493,7 @@ def _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, 
             return _qk_norm_rope_backward(name, dtype, q, k, dq_out, dk_out, freqs, positions, pos0, q_weight,
                                           k_weight, interleaved, eps, dq, dk, None)
     B, N, Hq, Hk, d, dev, qs, ks, rot, table = _qk_sides(q, k, freqs, positions, q_weight, k_weight, dtype)
+    _fits(name, B, N, Hq, Hk, d, rot)
     _want(dq_out, "dq_out", dtype, dev, (B, Hq, N, d))
     _want(dk_out, "dk_out", dtype, dev, (B, Hk, N, d))
     if dq is None:
@@ -546,6 +554,7 @@ def _gated_scan(name, dtype, gate, x, coupled, h0, lengths, h, h_last, stream):
         with _on(gate, stream):
             return _gated_scan(name, dtype, gate, x, coupled, h0, lengths, h, h_last, None)
     B, N, D, dev, gs, xs = _gated_sides(gate, x, h0, lengths, dtype)
+    _fits(name, B, N, D)
     if h is None:
         h = gate.new_empty(B, N, D)
     else:
@@ -582,6 +591,7 @@ def _gated_scan_backward(name, dtype, gate, x, h, dh, coupled, h0, lengths, dh_l
             return _gated_scan_backward(name, dtype, gate, x, h, dh, coupled, h0, lengths, dh_last, dgate, dx, dh0,
                                         None)
     B, N, D, dev, gs, xs = _gated_sides(gate, x, h0, lengths, dtype)
+    _fits(name, B, N, D)
     _want(h, "h", dtype, dev, (B, N, D))
     _want(dh, "dh", dtype, dev, (B, N, D))
     if dh_last is not None:
@@ -633,6 +643,7 @@ def _gated_step(name, dtype, gate, x, state, coupled, out, state_out, stream):
     if gate.dim() != 2:
         raise ValueError("gate, x must be [B, D]")
     B, D = shape = gate.shape
+    _fits(name, B, D)
     dev = gate.get_device()
     gs = _rows(gate, "gate", dtype, dev, shape)
     xs = _rows(x, "x", dtype, dev, shape)
@@ -678,6 +689,7 @@ def _shared_prefix_decode(name, dtype, q, k, v, prefix_state, k_cache, v_cache, 
         raise ValueError("q, k must be [B, H, d_k], v [B, H, d_v] and the caches [B, H, cap, d]")
     B, H, d_k = q.shape
     d_v, cap, dev = v.size(-1), k_cache.size(2), q.get_device()
+    _fits(name, B, H, d_k, d_v, cap)
     stride = _stride_of(d_k, d_v, n)
     if stride < 0:
         raise TaylorAttnError(TAYLOR_ERR_UNSUPPORTED, name)

@@ -208,3 +208,22 @@ assert all(torch.isfinite(t).all() for t in out if t is not None)
 """
     done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
     assert done.returncode == 0, done.stderr[-1500:]
+
+
+def test_sizes_past_32_bits_are_refused():
+    """Sizes that a C int does not hold (expanded tensors) are refused before anything is allocated or launched; they
+    were taken modulo 2^32, which left all but a few rows of the outputs as they were allocated."""
+    many, one = (1 << 32) + 1, torch.ones(1, device=DEV)
+    none = TA.rope_freqs(0)
+    rows, flat, cache = one.expand(1, many, 1), one.expand(many, 1), one.expand(1, 1, many, 1)
+    calls = [lambda: TA.taylor_attn_qk_norm_rope_f32(rows[..., None], rows[..., None], none),
+             lambda: TA.taylor_attn_qk_norm_rope_backward_f32(rows[..., None], rows[..., None], cache, cache, none),
+             lambda: TA.taylor_attn_gated_scan_f32(rows, rows),
+             lambda: TA.taylor_attn_gated_scan_backward_f32(rows, rows, rows, rows),
+             lambda: TA.taylor_attn_gated_step_f32(flat, flat, flat),
+             lambda: TA.taylor_attn_shared_prefix_decode_f32(one.view(1, 1, 1), one.view(1, 1, 1), one.expand(1, 1, 4), one,
+                                                             cache, cache, one, 2, TAU)]
+    for call in calls:
+        with pytest.raises(TA.TaylorAttnError) as refused:
+            call()
+        assert refused.value.status == TA.TAYLOR_ERR_UNSUPPORTED
