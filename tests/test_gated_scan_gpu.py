@@ -261,6 +261,30 @@ def test_states_may_be_written_over_the_ones_read(N, D):
     assert torch.equal(dgate, dgate2) and torch.equal(dx, dx2) and torch.equal(carry, dh0)
 
 
+@pytest.mark.parametrize("coupled", [True, False])
+def test_the_gradient_is_that_of_exact_states_within_their_rounding(coupled):
+    """bf16: dgate against the gradient that has the states in 64 bits.  The stored h_{t-1} is off by E (the module's
+    analysis) and half a step, and enters dgate times |G| a (1 - a); the kernel adds its own bound and a rounding."""
+    B, N, D = 2, 400, 72
+    gate, x, h0, dh, dl = _inputs("bf16", B, N, D, seed=21)
+    h, _ = TA.taylor_attn_gated_scan(gate, x, coupled=coupled, h0=h0)
+    dgate, dx, dh0 = TA.taylor_attn_gated_scan_backward(gate, x, h, dh, coupled=coupled, h0=h0, dh_last=dl, dh0=True)
+    g, xs, half = f64(gate), f64(x), _half("bf16")
+    want = L.gated_scan_grad(g, xs, f64(dh), coupled, f64(h0), None, f64(dl))
+    a, keep = L.sigmoid(g), L.sigmoid(-g)
+    states, _ = L.gated_scan(g, xs, coupled, f64(h0))
+    E, _ = _bounds(gate, x, coupled, h0, None)
+    before = np.concatenate([f64(h0)[:, None], states[:, :-1]], 1)
+    rounding = np.concatenate([np.zeros((B, 1, D)), E[:, :-1] + half * (np.abs(states[:, :-1]) + E[:, :-1])], 1)
+    m, e, limit = np.abs(f64(dl)), np.zeros((B, D)), np.zeros((B, N, D))
+    for t in reversed(range(N)):
+        m = m + np.abs(f64(dh[:, t]))
+        size = np.abs(before[:, t]) + rounding[:, t] + (np.abs(xs[:, t]) if coupled else 0.0)
+        limit[:, t] = a[:, t] * keep[:, t] * (m * rounding[:, t] + size * (e + 48 * U * m))
+        m, e = a[:, t] * m, a[:, t] * e + 24 * U * a[:, t] * m
+    _check(dgate, want[0], limit, half)
+
+
 def test_uncoupled_step():
     gate, x, h0, *_ = _inputs("f32", 4, 1, 20, seed=2)
     h, last = SCAN["f32"](gate, x, coupled=False, h0=h0, h_last=True)
