@@ -238,7 +238,11 @@ TAYLOR_API int taylor_attn_state_merge(const float* a, const float* b, float* ou
  * may be 0 (that side is left out).  Pointers need the alignment of their
  * elements only; rows whose length, strides and alignment allow it are moved
  * in up to 16-byte pieces.  For single tokens N = 1 gives [B][H][1][d], the
- * decode calls' layout.  No workspace. */
+ * decode calls' layout.  No workspace.
+ * The attention calls have one H: with Hk < Hq each key head is to be repeated
+ * for its query heads first.  And they expect unit norms: a row that weights
+ * have scaled by s makes their series one of tau times s, whose remainder grows
+ * with (tau s)^n / n!. */
 TAYLOR_API int taylor_attn_qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight,
                                         const int64_t* positions, int64_t pos0, const double* freqs, int rot,
                                         int interleaved, void* q_out, void* k_out, int B, int N, int Hq, int Hk,
@@ -259,7 +263,9 @@ TAYLOR_API int taylor_attn_qk_norm_rope_f32(const float* q, const float* k, cons
  * element at its own address) and, where not NULL, dq_weight and dk_weight
  * (fp32 [d]; only with that weight), summed over tokens and heads in fp32 in
  * an order that depends on the sizes alone.  The norm is recomputed from q and
- * k; a row of zeros with eps 0 has a zero gradient.  Workspace for the weight
+ * k; a row of zeros with eps 0 has a zero gradient.  dq and dk must not overlap
+ * the inputs or one another.  The attention has no gradient in this library:
+ * dq_out and dk_out come from the caller's own.  Workspace for the weight
  * gradients' partial sums as taylor_attn_prefill takes it. */
 TAYLOR_API int taylor_attn_qk_norm_rope_backward(const void* q, const void* k, const void* dq_out,
                                                  const void* dk_out, const float* q_weight, const float* k_weight,
@@ -315,7 +321,9 @@ TAYLOR_API int taylor_attn_gated_scan_f32(const float* gate, const float* x, con
  *     dgate_t = G_t (h_{t-1} - x_t | h_{t-1}) a_t (1 - a_t),  dh0 = a_0 G_0,
  * into dgate, dx (strides dgate_strides, dx_strides as above, every element at
  * its own address) and dh0 fp32 [B][D] (may be NULL, may be dh_last).  h_{t-1}
- * is the stored h, as rounded.  Rows past a length have zero gradients. */
+ * is the stored h, as rounded: with bf16 tensors dgate is off by half a step of
+ * h beside its own rounding.  dgate and dx must not overlap the inputs or one
+ * another.  Rows past a length have zero gradients. */
 TAYLOR_API int taylor_attn_gated_scan_backward(const void* gate, const void* x, const void* h, const void* dh,
                                                const float* h0, const int32_t* lengths, const float* dh_last,
                                                void* dgate, void* dx, float* dh0, int B, int N, int D,
@@ -334,7 +342,7 @@ TAYLOR_API int taylor_attn_gated_scan_backward_f32(const float* gate, const floa
 /* One token of the recurrence: gate, x [B][D] with the row strides
  * gate_stride, x_stride (elements), state_in fp32 [B][D]; writes the new state
  * to state_out (may be state_in) and, rounded to gate's type, to out [B][D]
- * (dense).  No workspace. */
+ * (dense), which must not overlap gate or x.  No workspace. */
 TAYLOR_API int taylor_attn_gated_step(const void* gate, const void* x, const float* state_in, float* state_out,
                                       void* out, int B, int D, int64_t gate_stride, int64_t x_stride, int coupled,
                                       cudaStream_t stream);
@@ -361,7 +369,9 @@ TAYLOR_API int taylor_attn_gated_step_f32(const float* gate, const float* x, con
  * leaves its caches alone and sets bit 32 of the device error word.  It pays
  * while a sequence's own tokens take fewer bytes than its state read and
  * written would: about 500 tokens a head at d_k 16, d_v 64, n 3 in bf16, 4,300
- * at d_k 64.  Workspace for the shared part as taylor_attn_prefill takes it. */
+ * at d_k 64.  The launch is laid out for cap tokens (lengths lie on the device):
+ * a cache far larger than the longest sequence costs up to a quarter more time.
+ * Workspace for the shared part as taylor_attn_prefill takes it. */
 TAYLOR_API int taylor_attn_shared_prefix_decode(const void* q, const void* k, const void* v,
                                                 const float* prefix_state, void* k_cache, void* v_cache,
                                                 const int32_t* lengths, float* out, int B, int H, int cap, int d_k,

@@ -384,9 +384,13 @@ constexpr int kBackCtas = 3;
 // two CTAs an SM ran 113 us (B4 N8192, 16 + 16 heads of 64, bf16, forward,
 // 268 MB); the ring at four CTAs 79 us, 79 % of the issue slots taken; pairs
 // in f32x2 instructions, row pointers that step and lane counts known at
-// compile time 58 us, 4.6 TB/s.  Backward 84 us without weights, 101 us with
-// (403 MB); at 4 CTAs it spills (152 us), at 2 it waits (109 us).  Ring depths
-// of 4 and 8 are within 2 %.
+// compile time 58 us.  Backward (403 MB), in the same way, 84 us without weights
+// and 101 us with; at 4 CTAs an SM it spills (152 us), at 2 it waits (109 us).
+// Ring depths of 4 and 8 are within 2 %.  All these are single launches; replayed
+// from a graph over two sets of buffers in turn, and with the weights' partial
+// sums joined by a launch that starts early, it takes now 54 us forward (5.0
+// TB/s), 84 us backward (4.8) and 94 us with weights (4.3); fp32 91, 130 and 133
+// us (5.9 to 6.2 TB/s).
 template <typename T, int VE, int LPR, bool BWD>
 __global__ void __launch_bounds__(256, BWD ? kBackCtas : kCtas)
 qk_vec_kernel(const __grid_constant__ QkArgs a, int lpr, int tok, int slices, int tiles) {

@@ -237,8 +237,8 @@ prefix_state_kernel(const __grid_constant__ PrefixArgs a, int splits, int ctiles
 // order that depends on the sizes alone.
 //
 // The cache's bytes bound it: 64 sequences of 16 heads, d 64 and 64, up to
-// 1,024 own tokens (144 MB) take 40 us with the shared part beside them, 3.6
-// TB/s; tokens in registers 68 us, with selects on every token 55 us.  What is
+// 1,024 own tokens (144 MB) take 40 us on the device with the shared part beside
+// them, 3.6 TB/s; tokens in registers 68 us, with selects on every token 55 us.  What is
 // left is the start and end of each CTA (2 to 4 us of some 15).
 constexpr int kUnroll = 2;  // tokens of eight lanes in a step
 
@@ -256,7 +256,7 @@ constexpr int ahead() {
 // CTAs of NW warps that the compiler is to leave registers for on an SM: seven
 // of four warps or three of eight, one where a lane's 32 columns and more need
 // them, and no more than fit into 228 KB with their rings, sums (below) and the
-// 1 KB that each CTA costs.  fp32, d_v 128 lets four to six CTAs of four warps
+// 1 KB that each CTA costs.  fp32, d_v 128 lets four or five CTAs of four warps
 // in; held to seven's 72 registers it took 22.6 us (64 sequences of 16 heads, d
 // 20, up to 200 tokens) and 23.8 us (d 64), with 86 and 96 registers 21.6 and
 // 23.5 us.
@@ -604,7 +604,11 @@ cudaError_t launch_prefix(PrefixArgs& a, cudaStream_t stream) {
     // 1,024 heads of up to 512 tokens, d 16, 17.0 us, at eight warps 19; 4,096 of
     // up to 512, d 64, 90 and 99 us), else eight (a long one would still run
     // when the others are done: 1,024 of up to 1,024, d 64, 44 and 39 us), and
-    // while that leaves each 256 tokens a cluster of CTAs
+    // while that leaves each 256 tokens a cluster of CTAs.  The lengths lie on the
+    // device, so the capacity stands for the longest: a cache of four times that
+    // costs up to a quarter (1,024 heads of up to 512, d 16, 17.3 and 19.2 us;
+    // 4,096 of up to 256, d 64, 65 and 81 us; 136 of up to 300, n 5 in fp32, 15.3
+    // and 18.2 us)
     const int64_t heads = (int64_t)a.B * a.H;
     const bool many = heads >= 2 * (int64_t)sms && (int64_t)a.cap * (a.d + a.dv) * (int64_t)sizeof(T) <= 192 * 1024;
     int64_t cluster = (int64_t)sms * 4 / heads, room = ((int64_t)a.cap + 255) / 256;
