@@ -119,12 +119,13 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 //
 // Memory bounds the operator, 6 B a value forward and 12 B backward in bf16;
 // this kernel is bound by instructions and the latency of its rounds: 25 and
-// 49 instructions a value, issue slots 58 to 61 % taken at 14 warps an SM.  B4 N8192
-// D1024 bf16: 50 us forward (4.0 TB/s), 87 us backward (4.6 TB/s), replayed from
-// a graph over two sets of buffers in turn (fp32 93 and 149 us); as single
-// launches 52 and 91 us, and with checks on every token, scalar arithmetic and a
-// cluster barrier a round 73 and 126 us; one thread a channel 9.8 ms for both.  A third stage in flight, or
-// 16-byte copies shared by two lanes, gain nothing.
+// 49 instructions a value, issue slots 58 to 61 % taken at 14 warps an SM.
+// B4 N8192 D1024 bf16: 50 us forward (4.0 TB/s), 87 us backward (4.6 TB/s),
+// replayed from a graph over two sets of buffers in turn (fp32 93 and 149 us).
+// As single launches 52 and 91 us; with checks on every token, scalar
+// arithmetic and a cluster barrier a round 73 and 126 us; one thread a channel
+// 9.8 ms for both.  A third stage in flight, or 16-byte copies shared by two
+// lanes, gain nothing.
 //
 // The CTAs of a cluster run at the same time, and each sends before it waits.
 // The totals' buffers alternate: a CTA sends those of round i + 2 only after it
