@@ -371,6 +371,8 @@ TAYLOR_API int taylor_attn_gated_step_f32(const float* gate, const float* x, con
  * written would: about 500 tokens a head at d_k 16, d_v 64, n 3 in bf16, 4,300
  * at d_k 64.  The launch is laid out for cap tokens (lengths lie on the device):
  * a cache far larger than the longest sequence costs up to a quarter more time.
+ * An infinity in q or prefix_state makes the outputs that it reaches NaN: the
+ * shared product takes its factors in two parts, and parts of infinities cancel.
  * Workspace for the shared part as taylor_attn_prefill takes it. */
 TAYLOR_API int taylor_attn_shared_prefix_decode(const void* q, const void* k, const void* v,
                                                 const float* prefix_state, void* k_cache, void* v_cache,
